@@ -389,6 +389,95 @@ esa_status_t esa_sparse_attn_varlen(const void* q, const void* k, const void* v,
 size_t esa_sparse_attn_varlen_workspace_size(int32_t batch, int64_t n_cap, int32_t hq, int32_t hkv,
                                              int32_t head_dim, esa_dtype_t dt, int32_t lists, esa_params_t p);
 
+/* ----------------------------------------------------- 8-bit key/value cache -- */
+
+/* A cache that holds keys and values as 8-bit codes with one fp32 scale for each block of
+ * `block` tokens and head (decode is bound by reading the attended rows: half the bytes of
+ * a bf16 cache, and half its memory). The value of a code is code * scale.
+ *   k, v:             [batch, n_cap, hkv, head_dim] codes, one byte each (16-byte aligned)
+ *   k_scale, v_scale: [batch, ceil(n_cap / block), hkv] fp32
+ *   format:           ESA_Q8_E4M3 (4 exponent and 3 mantissa bits, +-448) or
+ *                     ESA_Q8_INT8 (-127 .. 127)
+ *   block:            16, 32, 64 or 128;  head_dim: 64 or 128;  n_cap < 2^31
+ * All buffers are the caller's; nothing needs to be initialised before the first write of
+ * a sequence at position 0 (or at any multiple of block). */
+typedef enum { ESA_Q8_E4M3 = 0, ESA_Q8_INT8 = 1 } esa_q8_format_t;
+
+typedef struct {
+  void* k;
+  float* k_scale;
+  void* v;
+  float* v_scale;
+  int64_t n_cap;
+  int32_t batch, hkv, head_dim;
+  int32_t block;
+  int32_t format;
+} esa_cache_q8_t;
+
+/* esa_cache_write_q8 - quantise new key and value rows into positions [start, start +
+ * rows) of every sequence. A block that receives rows gets the scale
+ *   s' = max(s, 2^E),  2^E the smallest power of two >= 2^-100 with max |new x| <= qmax 2^E
+ * (per operand and head; s: the block's scale if it held rows before `start`, else 0;
+ * qmax 448 or 127). New rows become round(x / s'), the block's rows before `start`
+ * round(code * s / s') where s' > s (nearest, ties to even). Both divisions are by a power
+ * of two, so codes and values are defined to the bit. Rows at or behind start + rows keep
+ * their codes and count as empty: a later write there decides the scale again.
+ *   k, v: rows of [hkv, head_dim], dtype dt (ESA_F32 or ESA_BF16); row r of sequence b at
+ *         element b * batch_stride + r * row_stride (each row contiguous; strides give
+ *         16-byte aligned rows, so slices of a fused projection can be passed)
+ * A NaN is written as 0 and an infinity as the largest code of a block scaled by its
+ * finite values; esa_device_status() then reports ESA_ERR_INVALID_ARG. rows = 0 is a no-op. */
+esa_status_t esa_cache_write_q8(const void* k, const void* v, esa_dtype_t dt, int64_t rows,
+                                int64_t k_batch_stride, int64_t k_row_stride, int64_t v_batch_stride,
+                                int64_t v_row_stride, esa_cache_q8_t cache, int64_t start, void* stream);
+
+/* esa_cache_write_q8_varlen - the same for sequences of different lengths: sequence b,
+ * holding seq_len[b] tokens with the new ones, gets its rows 0 .. n_b - 1 at positions
+ * [seq_len[b] - n_b, seq_len[b]).
+ *   seq_len: device int64 [batch];  new_len: NULL (n_b = rows) or device int64 [batch]
+ * n_b = 0 leaves sequence b as it was (whatever its seq_len). Lengths that do not fit
+ * (n_b outside [0, rows], seq_len[b] outside [n_b, n_cap]) do too, and are recorded for
+ * esa_device_status(). */
+esa_status_t esa_cache_write_q8_varlen(const void* k, const void* v, esa_dtype_t dt, int64_t rows,
+                                       int64_t k_batch_stride, int64_t k_row_stride, int64_t v_batch_stride,
+                                       int64_t v_row_stride, esa_cache_q8_t cache, const int64_t* seq_len,
+                                       const int64_t* new_len, void* stream);
+
+/* esa_cache_read_q8 - rows of the cache as values (code * scale, rounded to dt; exact for
+ * scales that esa_cache_write_q8 wrote).
+ *   idx:   NULL: row r of the result is position start + r (0 <= start, start + rows <=
+ *          n_cap); else device int32 [batch, rows] positions, in any order and repeated at
+ *          will; one outside [0, n_cap) (the -1 of a selection's padding) gives zeros
+ *   k_out, v_out: [batch, rows, hkv, head_dim] of dtype dt, 32-byte aligned; either may be
+ *          NULL (not wanted) */
+esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows, const int32_t* idx,
+                               void* k_out, void* v_out, esa_dtype_t dt, void* stream);
+
+/* esa_sparse_attn_q8 - esa_sparse_attn (lists 1) or esa_sparse_attn_heads (lists == hkv)
+ * over an 8-bit cache: attention of queries at positions [c0, c0 + lq) over initial +
+ * idx[:count] + local tokens, causal in the chunk, on the values of the cache.
+ *   q, o:       [batch, lq, hq, head_dim] of dtype dt (ESA_F32 or ESA_BF16)
+ *   idx, count: [batch, lists, p.topk] and [batch, lists] int32, as the selections write them
+ *   lse:        NULL or [batch, lq, hq] fp32
+ * Scales may be any positive numbers below 2^121. hq is a multiple of hkv; no limit on
+ * their ratio. Codes are exact in the products; softmax weights are rounded to f16 (bf16
+ * for a chunk on the tensor-core path, see the workspace), and not at all for fp32 (22
+ * bits). The workspace (esa_sparse_attn_q8_workspace_size bytes, 256-byte aligned) holds a
+ * chunk's keys and values as bf16 (bf16, head_dim 128, hq / hkv in {1, 2, 4, 8} and
+ * lq * hq / hkv >= 64); 0 bytes otherwise. Other errors as for esa_sparse_attn. */
+esa_status_t esa_sparse_attn_q8(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, int32_t lq, int64_t c0,
+                                int32_t hq, const int32_t* idx, const int32_t* count, int32_t lists,
+                                esa_params_t p, float scale, void* o, float* lse, void* workspace,
+                                size_t ws_bytes, void* stream);
+size_t esa_sparse_attn_q8_workspace_size(int32_t batch, int32_t lq, int64_t c0, int32_t hq, int32_t hkv,
+                                         int32_t head_dim, esa_dtype_t dt, esa_params_t p);
+
+/* esa_sparse_attn_q8_varlen - the same for one query per sequence at its own position
+ * seq_len[b] - 1 (see the variable-length decode batches above). Needs no workspace. */
+esa_status_t esa_sparse_attn_q8_varlen(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, const int64_t* seq_len,
+                                       int32_t hq, const int32_t* idx, const int32_t* count, int32_t lists,
+                                       esa_params_t p, float scale, void* o, float* lse, void* stream);
+
 /* ------------------------------------------- offline fit of the compression maps -- */
 
 /* esa_gram - the Gram matrix G = X^T X of calibration rows X [n, dim] (bf16, rows

@@ -31,6 +31,15 @@ class EsaParams(ctypes.Structure):
                 ("eps", ctypes.c_int32), ("clamp_c", ctypes.c_float)]
 
 
+class EsaCacheQ8(ctypes.Structure):
+    """esa_cache_q8_t: the buffers, sizes and format of an 8-bit key/value cache."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_cap", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
 SIGNATURES = {
     "esa_compress": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _vp]),
     "esa_compress_pack_size": (_sz, [_i32, _i32, _i32]),
@@ -82,6 +91,16 @@ SIGNATURES = {
     "esa_sparse_attn_varlen": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _i32, _i64, _vp, _i32, _i32, _i32, _vp,
                                               _vp, _i32, EsaParams, _f32, _vp, _vp, _vp, _sz, _vp]),
     "esa_sparse_attn_varlen_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32, ctypes.c_int, _i32, EsaParams]),
+    "esa_cache_write_q8": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, EsaCacheQ8, _i64,
+                                          _vp]),
+    "esa_cache_write_q8_varlen": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, EsaCacheQ8,
+                                                 _vp, _vp, _vp]),
+    "esa_cache_read_q8": (ctypes.c_int, [EsaCacheQ8, _i64, _i64, _vp, _vp, _vp, ctypes.c_int, _vp]),
+    "esa_sparse_attn_q8": (ctypes.c_int, [_vp, ctypes.c_int, EsaCacheQ8, _i32, _i64, _i32, _vp, _vp, _i32, EsaParams,
+                                          _f32, _vp, _vp, _vp, _sz, _vp]),
+    "esa_sparse_attn_q8_workspace_size": (_sz, [_i32, _i32, _i64, _i32, _i32, _i32, ctypes.c_int, EsaParams]),
+    "esa_sparse_attn_q8_varlen": (ctypes.c_int, [_vp, ctypes.c_int, EsaCacheQ8, _vp, _i32, _vp, _vp, _i32, EsaParams,
+                                                 _f32, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -435,6 +454,204 @@ def sparse_attn_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_le
                                          _ptr(lse) if want_lse else None, wp, wn, _stream()),
            "esa_sparse_attn_varlen")
     return out, (lse if want_lse else None)
+
+
+Q8_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}     # code dtype -> esa_q8_format_t
+
+
+class CacheQ8:
+    """An 8-bit key/value cache: codes k, v [B, n_cap, Hkv, D] (torch.float8_e4m3fn or
+    torch.int8) and scales k_scale, v_scale [B, ceil(n_cap / block), Hkv] fp32, one for each
+    block of tokens and head; a value is code * scale. The tensors are the caller's (see
+    cache_q8 for new ones), are checked once, here, and stay the ones of this cache."""
+
+    __slots__ = ("_k", "_k_scale", "_v", "_v_scale", "_c")
+
+    def __init__(self, k: torch.Tensor, k_scale: torch.Tensor, v: torch.Tensor, v_scale: torch.Tensor, block: int):
+        _dev(k, k_scale, v, v_scale)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in Q8_FORMATS:
+            raise ValueError("k and v must be [B, n_cap, Hkv, D] of one dtype, torch.float8_e4m3fn or torch.int8")
+        if block not in (16, 32, 64, 128):
+            raise ValueError("block must be 16, 32, 64 or 128")
+        b, n_cap, hkv, d = k.shape
+        want = (b, (n_cap + block - 1) // block, hkv)
+        for t in (k_scale, v_scale):
+            if t.dtype != torch.float32 or t.shape != want:
+                raise ValueError(f"scales must be float32 {list(want)}")
+        if len({t.device for t in (k, k_scale, v, v_scale)}) > 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self._k, self._k_scale, self._v, self._v_scale = k, k_scale, v, v_scale
+        self._c = EsaCacheQ8(_ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), n_cap, b, hkv, d, block,
+                             Q8_FORMATS[k.dtype])
+
+    k = property(lambda self: self._k)
+    k_scale = property(lambda self: self._k_scale)
+    v = property(lambda self: self._v)
+    v_scale = property(lambda self: self._v_scale)
+    block = property(lambda self: self._c.block)
+    device = property(lambda self: self._k.device)
+
+
+def cache_q8(batch: int, n_cap: int, hkv: int, head_dim: int, dtype: torch.dtype = torch.float8_e4m3fn,
+             block: int = 64, device="cuda") -> CacheQ8:
+    """A new, empty CacheQ8 (codes and scales zero)."""
+    def codes():
+        return torch.zeros((batch, n_cap, hkv, head_dim), dtype=torch.uint8, device=device).view(dtype)
+
+    def scales():
+        return torch.zeros((batch, (n_cap + block - 1) // block, hkv), dtype=torch.float32, device=device)
+    return CacheQ8(codes(), scales(), codes(), scales(), block)
+
+
+def _q8_call(cache: CacheQ8, where: str, *args):
+    """Call `where` with args and the current stream of the cache's device, under that
+    device."""
+    dev = cache._k.device
+    fn = getattr(load(), where)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    _check(st, where)
+
+
+def _q8_tensor(t: torch.Tensor, name: str, cache: CacheQ8, dtype, shape):
+    """t as an argument of a call on the cache: its device, dtype, shape, contiguous."""
+    if t.device != cache._k.device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the cache's device")
+
+
+def _q8_rows(x: torch.Tensor, name: str, cache: CacheQ8):
+    """New rows [B, T, Hkv, D]: batch and row strides free, each row contiguous."""
+    c = cache._c
+    if x.device != cache._k.device:
+        raise ValueError(f"{name} must be on the cache's device (no CPU path)")
+    if x.dim() != 4 or x.shape[0] != c.batch or x.shape[2] != c.hkv or x.shape[3] != c.head_dim:
+        raise ValueError(f"{name} must be [B, T, Hkv, D] = [{c.batch}, T, {c.hkv}, {c.head_dim}]")
+    if x.stride(3) != 1 or (c.hkv > 1 and x.stride(2) != c.head_dim):
+        raise ValueError(f"each row of {name} must be contiguous [Hkv, D]")
+
+
+def _q8_write(where: str, cache: CacheQ8, k: torch.Tensor, v: torch.Tensor, *tail):
+    _q8_rows(k, "k", cache)
+    _q8_rows(v, "v", cache)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    # a stride that no second row or sequence uses may be anything: pass one that is aligned
+    kb, kr, vb, vr = (x.stride(i) if x.shape[i] > 1 else c for x in (k, v)
+                      for i, c in ((0, 0), (1, cache._c.hkv * cache._c.head_dim)))
+    _q8_call(cache, where, _ptr(k), _ptr(v), _dtype_code(k), k.shape[1], kb, kr, vb, vr, cache._c, *tail)
+
+
+def cache_write_q8(cache: CacheQ8, k: torch.Tensor, v: torch.Tensor, start: int) -> None:
+    """esa_cache_write_q8: quantise k, v [B, T, Hkv, D] (f32 or bf16; rows may be strided)
+    into positions [start, start + T) of every sequence of the cache."""
+    _q8_write("esa_cache_write_q8", cache, k, v, start)
+
+
+def cache_write_q8_varlen(cache: CacheQ8, k: torch.Tensor, v: torch.Tensor, seq_len: torch.Tensor,
+                          new_len: Optional[torch.Tensor] = None) -> None:
+    """esa_cache_write_q8_varlen: sequence b's rows (the first new_len[b] of its T, or all)
+    into positions [seq_len[b] - new_len[b], seq_len[b]). Lengths: int64 [B] on the device."""
+    b = cache._c.batch
+    _q8_tensor(seq_len, "seq_len", cache, torch.int64, (b,))
+    if new_len is not None:
+        _q8_tensor(new_len, "new_len", cache, torch.int64, (b,))
+    _q8_write("esa_cache_write_q8_varlen", cache, k, v, _ptr(seq_len), _ptr(new_len))
+
+
+def cache_read_q8(cache: CacheQ8, start: int = 0, rows: Optional[int] = None, idx: Optional[torch.Tensor] = None,
+                  dtype: torch.dtype = torch.bfloat16, want_k: bool = True, want_v: bool = True,
+                  k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None):
+    """esa_cache_read_q8: the values of positions [start, start + rows) (to the end of the
+    cache without rows), or of idx [B, n] int32 (outside the cache: zeros).
+    Returns (k [B, n, Hkv, D] or None, v or None) of dtype f32 or bf16."""
+    c = cache._c
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dtype}")
+    if idx is not None:
+        if start != 0 or rows is not None:
+            raise ValueError("idx excludes start and rows")
+        n = idx.shape[-1]
+        _q8_tensor(idx, "idx", cache, torch.int32, (c.batch, n))
+    else:
+        n = c.n_cap - start if rows is None else rows
+        if start < 0 or n < 0 or start + n > c.n_cap:
+            raise ValueError("need 0 <= start and start + rows <= n_cap")
+    shape = (c.batch, n, c.hkv, c.head_dim)
+    got = []
+    for out, want, name in ((k_out, want_k, "k_out"), (v_out, want_v, "v_out")):
+        if not want:
+            out = None
+        elif out is None:
+            out = torch.empty(shape, dtype=dtype, device=cache._k.device)
+        else:
+            _q8_tensor(out, name, cache, dtype, shape)
+        got.append(out)
+    _q8_call(cache, "esa_cache_read_q8", c, start, n, _ptr(idx), _ptr(got[0]), _ptr(got[1]),
+             ESA_BF16 if dtype == torch.bfloat16 else ESA_F32)
+    return got[0], got[1]
+
+
+def _q8_attn_args(q, cache: CacheQ8, idx, count, p: EsaParams, want_lse, out, lse):
+    """Checks and outputs shared by the attention calls; returns (lists, out, lse)."""
+    c = cache._c
+    if q.dim() != 4 or q.shape[0] != c.batch or q.shape[3] != c.head_dim:
+        raise ValueError(f"q must be [B, Lq, Hq, D] = [{c.batch}, Lq, Hq, {c.head_dim}]")
+    if q.device != cache._k.device or not q.is_contiguous():
+        raise ValueError("q must be contiguous and on the cache's device (no CPU path)")
+    lists = count.shape[1] if count.dim() == 2 else 1
+    if count.dim() == 2:
+        _q8_tensor(count, "count", cache, torch.int32, (c.batch, lists))
+        _q8_tensor(idx, "idx", cache, torch.int32, (c.batch, lists, p.topk))
+    else:
+        _q8_tensor(count, "count", cache, torch.int32, (c.batch,))
+        _q8_tensor(idx, "idx", cache, torch.int32, (c.batch, p.topk))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _q8_tensor(out, "out", cache, q.dtype, q.shape)
+    if not want_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    else:
+        _q8_tensor(lse, "lse", cache, torch.float32, q.shape[:3])
+    return lists, out, lse
+
+
+def sparse_attn_q8_workspace_size(batch, lq, c0, hq, hkv, d, dtype_code, p: EsaParams) -> int:
+    return load().esa_sparse_attn_q8_workspace_size(batch, lq, c0, hq, hkv, d, dtype_code, p)
+
+
+def sparse_attn_q8(q: torch.Tensor, cache: CacheQ8, c0: int, idx: torch.Tensor, count: torch.Tensor, p: EsaParams,
+                   scale: float = 0.0, want_lse: bool = False, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """esa_sparse_attn_q8: q [B, Lq, Hq, D] at positions [c0, c0 + Lq) over the cache's
+    initial + idx[:count] + local tokens; idx [B, topk], count [B] int32, or [B, L, topk] and
+    [B, L] with L = 1 or Hkv (a list per KV head). Returns (o like q, lse [B, Lq, Hq] or None)."""
+    lists, out, lse = _q8_attn_args(q, cache, idx, count, p, want_lse, out, lse)
+    c, (b, lq, hq, d), dt = cache._c, q.shape, _dtype_code(q)
+    ws = _workspace(sparse_attn_q8_workspace_size(b, lq, c0, hq, c.hkv, d, dt, p), q.device, workspace)
+    wp, wn = _ws_ptr(ws)
+    _q8_call(cache, "esa_sparse_attn_q8", _ptr(q), dt, c, lq, c0, hq, _ptr(idx), _ptr(count), lists, p, scale,
+             _ptr(out), _ptr(lse), wp, wn)
+    return out, lse
+
+
+def sparse_attn_q8_varlen(q: torch.Tensor, cache: CacheQ8, seq_len: torch.Tensor, idx: torch.Tensor,
+                          count: torch.Tensor, p: EsaParams, scale: float = 0.0, want_lse: bool = False,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """esa_sparse_attn_q8_varlen: one query per sequence, q [B, 1, Hq, D], at position
+    seq_len[b] - 1 (int64 [B] on the device). Lists and results as sparse_attn_q8."""
+    lists, out, lse = _q8_attn_args(q, cache, idx, count, p, want_lse, out, lse)
+    if q.shape[1] != 1:
+        raise ValueError("one query per sequence")
+    _q8_tensor(seq_len, "seq_len", cache, torch.int64, (cache._c.batch,))
+    _q8_call(cache, "esa_sparse_attn_q8_varlen", _ptr(q), _dtype_code(q), cache._c, _ptr(seq_len), q.shape[2],
+             _ptr(idx), _ptr(count), lists, p, scale, _ptr(out), _ptr(lse))
+    return out, lse
 
 
 def gram(x: torch.Tensor, workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -1,0 +1,494 @@
+// attn_q8.cuh - exact attention of few queries over the initial + selected + local tokens
+// of an 8-bit cache (ESA write-up: implementation and final-attention paragraphs - global
+// part = initial + selected tokens, window part = local tokens, one softmax).
+//
+// With codes kc, vc and block scales a, b the logits and the output of a query row are
+//   x_j = c (q . kc_j) a_j,    l = sum_j 2^(x_j - m),    o = sum_j 2^(x_j + log2 b_j - m) vc_j / l
+// (c = softmax scale * log2 e), so the scales never touch the codes: they multiply one
+// logit and add to one exponent per key. Both products run on the tensor cores as
+// m16n8k16 f16 MMAs with fp32 accumulation, and an e4m3 or int8 code is an exact f16:
+//   S^T [16 keys x 8 rows]  = Kc [16 x D] . Q^T       (A = codes, B = queries)
+//   O^T [D x 8 rows]       += Vc^T [D x 16 keys] . W^T (A = codes transposed, B = weights)
+// Keys and dims are the M dimension and the query rows N = 8, because a decode step has
+// only the G heads of a KV head as rows. A dot product does not mind the order of its
+// terms, so the fragments take their dims (K) and keys (V) in the order in which 16-byte
+// loads from global memory deliver them: no shared memory and no transposition in the
+// loop, only byte pairs of two keys brought side by side (prmt) and one conversion per
+// two codes. S^T becomes the B operand of the second product by movmatrix.
+// m is a reference, not the maximum: it is raised to max_j (x_j + log2 b_j) when that
+// exceeds it by 2^5, and W = 2^(.. - m + 10) <= 2^15 is rounded to f16 (relative 2^-11; a
+// weight under 2^-35 of the largest is lost, which 2^20 of them do not make visible). l
+// sums unrounded fp32 terms. fp32 queries go in as two f16 (q = hi + lo), and so do the
+// weights, for 22 bits of each.
+//
+// Bound by HBM: each attended code is read once. A warp streams 16 keys a step, 16 bytes a
+// lane and load, the next step's codes in flight under the present one's arithmetic. The
+// key list of a (sequence, KV head) is split over the warps of a CTA and over the CTAs of
+// a cluster; the parts meet in (distributed) shared memory, so there is no workspace, no
+// counter to clear and no second kernel.
+#pragma once
+#include "attn_tc.cuh"
+#include "cache_q8.cuh"
+#include "common.cuh"
+#include "keylist.cuh"
+
+namespace esa {
+
+constexpr int kQ8Warps = 8, kQ8Threads = kQ8Warps * 32;
+constexpr int kQ8Keys = 16;                     // keys of a warp's step
+constexpr float kQ8Head = 10.f, kQ8Lazy = 5.f;  // weights reach 2^(10 + 5), below f16's 2^16
+
+struct AttnQ8Args {
+  const void* q;            // [B, Lq, Hq, D]
+  const uint8_t* k;         // [B, n_cap, Hkv, D]
+  const uint8_t* v;
+  const float* ks;          // [B, nblk, Hkv]
+  const float* vs;
+  void* o;                  // [B, Lq, Hq, D]
+  float* lse;               // [B, Lq, Hq] or null
+  KeyList keys;
+  int64_t n_cap, nblk, c0;
+  int lq, hq, hkv, G;
+  int lists, bshift;
+  int hc;                   // KV heads of a CTA (1, 2, 4 or 8; divides hkv)
+  int tiles;                // row tiles of a KV head
+  float scale_log2;
+};
+
+template <int NT, int D>
+__host__ __device__ constexpr int q8_row_floats() { return D + 4; }     // o, then padding
+template <int NT, int D>
+__host__ __device__ constexpr int q8_smem_bytes() {
+  // the warps' partial rows; (m, l) of every warp row; (m, l) of every merged row
+  return (kQ8Warps * 8 * NT * q8_row_floats<NT, D>() + 4 * kQ8Warps * 8 * NT) * 4;
+}
+
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The four codes of word w as two f16 pairs. K: word = 4 dims of one key; the pairs are
+// the dims (0, 1), (2, 3) for e4m3 and (0, 2), (1, 3) for int8 (q8_pair_dim).
+template <int FMT>
+__device__ __forceinline__ void q8_pairs(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  if constexpr (FMT == kQ8E4M3) {
+    p0 = e4m3x2_to_f16x2((uint16_t)w);
+    p1 = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+  } else {
+    // 0x6400 | (c + 128) is the f16 1024 + 128 + c: exact, and so is the difference
+    const uint32_t t0 = (w & 0x00ff00ffu) ^ 0x64806480u, t1 = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(p0) : "r"(t0), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(p1) : "r"(t1), "r"(0x64806480u));
+  }
+}
+// dim (0..3 of a word) that element e (0, 1) of pair p holds
+template <int FMT>
+__host__ __device__ constexpr int q8_pair_dim(int p, int e) { return FMT == kQ8E4M3 ? 2 * p + e : p + 2 * e; }
+
+// Words wa, wb: the same 4 dims of two keys. dims[d] = (key a, key b) of dim d as f16.
+template <int FMT>
+__device__ __forceinline__ void q8_transpose(uint32_t wa, uint32_t wb, uint32_t* dims) {
+  if constexpr (FMT == kQ8E4M3) {
+    q8_pairs<FMT>(__byte_perm(wa, wb, 0x5140), dims[0], dims[1]);
+    q8_pairs<FMT>(__byte_perm(wa, wb, 0x7362), dims[2], dims[3]);
+  } else {
+    q8_pairs<FMT>(__byte_perm(wa, wb, 0x5410), dims[0], dims[1]);
+    q8_pairs<FMT>(__byte_perm(wa, wb, 0x7632), dims[2], dims[3]);
+  }
+}
+
+// log2 of a positive scale; an integer, exactly, for a power of two. Scales under 2^-120
+// (zero among them) count as 2^-120.
+__device__ __forceinline__ float q8_log2(float s) {
+  const uint32_t u = __float_as_uint(fmaxf(s, 0x1p-120f));
+  const uint32_t mant = u & 0x7fffffu;
+  const float e = (float)((int)(u >> 23) - 127);
+  return mant ? e + __log2f(__uint_as_float(mant | 0x3f800000u)) : e;
+}
+
+// A power of two f (and its reciprocal's log2) that brings amax to [2^13, 2^14): queries
+// of any range fit f16, and the elements that matter stay normal there.
+__device__ __forceinline__ int q8_query_exp(float amax) {
+  const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
+  return min(13 - e, 100);
+}
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* f) {
+  if constexpr (sizeof(T) == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 a = bf16x2_to_float2(v.x), b = bf16x2_to_float2(v.y);
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+  } else {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  }
+}
+
+// grid (cluster size, (Hkv / hc) * tiles, B), cluster (cluster size, 1, 1).
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1) attn_q8_kernel(const AttnQ8Args a) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int ROWS = 8 * NT;
+  constexpr int KC = D / 64;             // 16-byte pieces of a key row a lane takes (K)
+  constexpr int VW = D / 32;             // words of a value row a lane takes (V)
+  constexpr int RF = q8_row_floats<NT, D>();
+  extern __shared__ __align__(16) float q8sm[];
+  float* const sm_o = q8sm;                                    // [warp][ROWS][RF]
+  float* const sm_ml = sm_o + kQ8Warps * ROWS * RF;            // [warp][ROWS][2]
+  float* const sm_fin = sm_ml + 2 * kQ8Warps * ROWS;           // [head slot][ROWS][2]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int hc = a.hc, kw = kQ8Warps / hc;
+  const int hs = warp & (hc - 1), kp = warp / hc;
+  const int hg = blockIdx.y / a.tiles, tile = blockIdx.y - hg * a.tiles;
+  const int g = hg * hc + hs, b = blockIdx.z;
+  const int rank = blockIdx.x, csize = gridDim.x;
+
+  const int list = a.lists > 1 ? b * a.lists + g : b;
+  KeyList kl = a.keys;
+  const int64_t c0 = kl.vl.len ? kl.resolve(b, 704) : a.c0;
+  const int cnt = min(max(kl.count[list], 0), (int)kl.idx_stride);
+  const int n_prior = (int)(kl.ni + cnt + (c0 - kl.lo));       // keys before the first query's own
+  const int r0 = tile * ROWS, nrow = min(ROWS, a.lq * a.G - r0);
+  const int i_first = r0 / a.G;
+  const int n_keys = n_prior + (r0 + nrow - 1) / a.G + 1;      // that the tile's last row attends
+  const int n_all = n_prior + i_first + 1;                     // that every row of the tile attends
+  const int steps = (n_keys + kQ8Keys - 1) / kQ8Keys;
+  const int s_end = (int)((int64_t)steps * (rank + 1) / csize);
+  const int s_beg = (int)((int64_t)steps * rank / csize) + kp;
+
+  // ---- queries: B fragments, row gid of each group of 8, dims in the order of K's words
+  uint32_t qf[NT][KC][4][2], ql[F32 ? NT : 1][KC][4][2];
+  float xs[NT][2];                                             // logit factors of rows 2 tig, 2 tig + 1
+  int lim[NT][2];                                              // first key they do not attend
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = min(r0 + nt * 8 + gid, a.lq * a.G - 1);
+    const int i = r / a.G, hl = r - i * a.G;
+    const T* qp = static_cast<const T*>(a.q) + (((int64_t)b * a.lq + i) * a.hq + g * a.G + hl) * D;
+    float f[KC][4][4];
+    float mx = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        load4(qp + c * 64 + tig * 16 + w * 4, f[c][w]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(f[c][w][e]));
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int qe = q8_query_exp(mx);
+    const float up = __uint_as_float((uint32_t)(qe + 127) << 23);
+    const float down = a.scale_log2 * __uint_as_float((uint32_t)(127 - qe) << 23);
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const float x0 = f[c][w][q8_pair_dim<FMT>(p, 0)] * up, x1 = f[c][w][q8_pair_dim<FMT>(p, 1)] * up;
+          qf[nt][c][w][p] = f16x2_rn(x0, x1);
+          if constexpr (F32) {
+            const float2 h = f16x2_to_float2(qf[nt][c][w][p]);
+            ql[nt][c][w][p] = f16x2_rn(x0 - h.x, x1 - h.y);
+          }
+        }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      xs[nt][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * tig + j));
+      lim[nt][j] = n_prior + min(r0 + nt * 8 + 2 * tig + j, a.lq * a.G - 1) / a.G + 1;
+    }
+  }
+
+  // ---- the stream: positions two steps ahead, codes and scales one step ahead
+  const int64_t row_bytes = (int64_t)a.hkv * D;
+  const uint8_t* kb = a.k + (int64_t)b * a.n_cap * row_bytes + g * D + tig * 16;
+  const uint8_t* vb = a.v + (int64_t)b * a.n_cap * row_bytes + g * D + gid * (D / 8);
+  const float* sb = (lane < 16 ? a.ks : a.vs) + (int64_t)b * a.nblk * a.hkv + g;
+  const int32_t* ib = kl.idx + (int64_t)list * kl.idx_stride;
+  const int ni = (int)kl.ni, jump = (int)(kl.lo - kl.ni) - cnt;
+  auto position = [&](int s) -> int {              // of key slot lane % 16 of step s (a key behind the list: its last)
+    const int t = min(s * kQ8Keys + (lane & 15), n_keys - 1);
+    int p = t < ni ? t : (t < ni + cnt ? __ldg(ib + t - ni) : t + jump);
+    return min(max(p, 0), (int)a.n_cap - 1);
+  };
+  uint4 kr[2][KC];
+  uint32_t vr[4][VW];
+  auto load_k = [&](int pos, uint4 (&k)[2][KC]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* p = kb + __shfl_sync(0xffffffffu, pos, gid + 8 * u) * row_bytes;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) k[u][c] = ld_stream16(p + c * 64);
+    }
+  };
+  auto load_v = [&](int pos, uint32_t (&v)[4][VW]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint8_t* p = vb + __shfl_sync(0xffffffffu, pos, 2 * tig + (u & 1) + 8 * (u >> 1)) * row_bytes;
+      if constexpr (VW == 4) {
+        const uint4 x = ld_stream16(p);
+        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+      } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        v[u][0] = x.x; v[u][1] = x.y;
+      }
+    }
+  };
+  auto load_s = [&](int pos) -> float { return __ldg(sb + (int64_t)(pos >> a.bshift) * a.hkv); };
+
+  float acc[2 * VW][NT][4];              // O^T tiles: dims (2 t, 2 t + 1) of the lane's D / 8, rows 2 tig, 2 tig + 1
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      m[nt][j] = -INFINITY;
+      l[nt][j] = 0.f;
+    }
+#pragma unroll
+  for (int t = 0; t < 2 * VW; ++t)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][nt][e] = 0.f;
+
+  float sc = 1.f;
+  int pos_n = 0;
+  if (s_beg < s_end) {
+    const int pos = position(s_beg);
+    load_k(pos, kr);
+    load_v(pos, vr);
+    sc = load_s(pos);
+    if (s_beg + kw < s_end) pos_n = position(s_beg + kw);
+  }
+  for (int s = s_beg; s < s_end; s += kw) {
+    const bool more = s + kw < s_end;
+    const float sc_cur = sc;
+    uint4 kn[2][KC];
+    if (more) {
+      load_k(pos_n, kn);
+      sc = load_s(pos_n);
+    }
+
+    // S^T = Kc Q^T, two chains of half the dims
+    float sx[NT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sx[nt][h][0] = sx[nt][h][1] = sx[nt][h][2] = sx[nt][h][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a0, a1, a2, a3;
+        const uint4 &ka = kr[0][c], &kbb = kr[1][c];
+        q8_pairs<FMT>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, a0, a2);
+        q8_pairs<FMT>(w == 0 ? kbb.x : w == 1 ? kbb.y : w == 2 ? kbb.z : kbb.w, a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(sx[nt][w & 1], a0, a1, a2, a3, qf[nt][c][w][0], qf[nt][c][w][1]);
+          if constexpr (F32) mma_f16(sx[nt][w & 1], a0, a1, a2, a3, ql[nt][c][w][0], ql[nt][c][w][1]);
+        }
+      }
+
+    // softmax: keys gid and gid + 8 (u), rows 2 tig and 2 tig + 1 (j)
+    const float lg = q8_log2(sc_cur);
+    float ka[2], lv[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      ka[u] = __shfl_sync(0xffffffffu, sc_cur, gid + 8 * u);
+      lv[u] = __shfl_sync(0xffffffffu, lg, 16 + gid + 8 * u);
+    }
+    const int t0 = s * kQ8Keys;
+    const bool cut = t0 + kQ8Keys > n_all;
+    float x[NT][2][2];
+    float top[NT][2];
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[nt][j][u] = (sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j]) * ka[u] * xs[nt][j];
+          if (cut && t0 + gid + 8 * u >= lim[nt][j]) x[nt][j][u] = -INFINITY;
+        }
+        float mx = fmaxf(x[nt][j][0] + lv[0], x[nt][j][1] + lv[1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        top[nt][j] = mx;
+        raise |= mx > m[nt][j] + kQ8Lazy;
+      }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float al[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mn = fmaxf(m[nt][j], top[nt][j]);
+          al[j] = mn == -INFINITY ? 1.f : fast_exp2(m[nt][j] - mn);
+          m[nt][j] = mn;
+          l[nt][j] *= al[j];
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * VW; ++t) {
+          acc[t][nt][0] *= al[0];
+          acc[t][nt][1] *= al[1];
+          acc[t][nt][2] *= al[0];
+          acc[t][nt][3] *= al[1];
+        }
+      }
+    }
+    uint32_t wf[NT][2], wl[F32 ? NT : 1][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float wt[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float mr = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          l[nt][j] += fast_exp2(x[nt][j][u] - mr);
+          wt[u][j] = fast_exp2(x[nt][j][u] + lv[u] - mr + kQ8Head);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t h = f16x2_rn(wt[u][0], wt[u][1]);
+        wf[nt][u] = movmatrix_t(h);
+        if constexpr (F32) {
+          const float2 hf = f16x2_to_float2(h);
+          wl[nt][u] = movmatrix_t(f16x2_rn(wt[u][0] - hf.x, wt[u][1] - hf.y));
+        }
+      }
+    }
+
+    // O^T += Vc^T W^T
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      uint32_t da[4], db[4];
+      q8_transpose<FMT>(vr[0][w], vr[1][w], da);       // keys 2 tig, 2 tig + 1
+      q8_transpose<FMT>(vr[2][w], vr[3][w], db);       // keys 2 tig + 8, 2 tig + 9
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(acc[2 * w + p][nt], da[2 * p], da[2 * p + 1], db[2 * p], db[2 * p + 1], wf[nt][0], wf[nt][1]);
+          if constexpr (F32)
+            mma_f16(acc[2 * w + p][nt], da[2 * p], da[2 * p + 1], db[2 * p], db[2 * p + 1], wl[nt][0], wl[nt][1]);
+        }
+    }
+    if (more) {
+      load_v(pos_n, vr);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < KC; ++c) kr[u][c] = kn[u][c];
+      if (s + 2 * kw < s_end) pos_n = position(s + 2 * kw);
+    }
+  }
+
+  // ---- the warp's rows to shared memory
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+      l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+      l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+      const int r = nt * 8 + 2 * tig + j;
+      if (r >= nrow) continue;
+      float* p = sm_o + (warp * ROWS + r) * RF + gid * (D / 8);
+#pragma unroll
+      for (int t = 0; t < 2 * VW; ++t)
+        *reinterpret_cast<float2*>(p + 2 * t) = make_float2(acc[t][nt][j], acc[t][nt][2 + j]);
+      if (gid == 0) *reinterpret_cast<float2*>(sm_ml + (warp * ROWS + r) * 2) = make_float2(m[nt][j], l[nt][j]);
+    }
+  __syncthreads();
+  // merge the key parts of each head inside the CTA: slot hs takes over warps hs + hc * kp
+  constexpr int Q = D / 4;
+  for (int it = threadIdx.x; it < hc * nrow * Q; it += kQ8Threads) {
+    const int d4 = it % Q, r = (it / Q) % nrow, h = it / Q / nrow;
+    float M = -INFINITY;
+    for (int u = 0; u < kw; ++u) M = fmaxf(M, sm_ml[((h + hc * u) * ROWS + r) * 2]);
+    const float mr = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < kw; ++u) {
+      const int wr = (h + hc * u) * ROWS + r;
+      const float c = fast_exp2(sm_ml[wr * 2] - mr);
+      const float4 o = *reinterpret_cast<const float4*>(sm_o + wr * RF + d4 * 4);
+      L += sm_ml[wr * 2 + 1] * c;
+      O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
+    }
+    *reinterpret_cast<float4*>(sm_o + (h * ROWS + r) * RF + d4 * 4) = O;     // read by this thread only
+    if (d4 == 0) *reinterpret_cast<float2*>(sm_fin + (h * ROWS + r) * 2) = make_float2(M, L);
+  }
+  if (csize > 1) cluster_sync_all();
+  else __syncthreads();
+  // merge the CTAs of the cluster: CTA `rank` writes every csize-th group of 256 items
+  for (int it = threadIdx.x + kQ8Threads * rank; it < hc * nrow * Q; it += kQ8Threads * csize) {
+    const int d4 = it % Q, r = (it / Q) % nrow, h = it / Q / nrow;
+    const uint32_t ml = smem_u32(sm_fin + (h * ROWS + r) * 2), oo = smem_u32(sm_o + (h * ROWS + r) * RF + d4 * 4);
+    float M = -INFINITY;
+    for (int u = 0; u < csize; ++u) M = fmaxf(M, __uint_as_float(ld_dsmem_u32(dsmem_map(ml, u))));
+    const float mr = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < csize; ++u) {
+      const uint2 z = ld_dsmem_u2(dsmem_map(ml, u));
+      const float4 o = ld_dsmem_f4(dsmem_map(oo, u));
+      const float c = fast_exp2(__uint_as_float(z.x) - mr);
+      L += __uint_as_float(z.y) * c;
+      O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
+    }
+    const int i = (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
+    const int64_t row = ((int64_t)b * a.lq + i) * a.hq + (hg * hc + h) * a.G + hl;
+    const float inv = 0x1p-10f / L;                                          // 2^-kQ8Head
+    T* dst = static_cast<T*>(a.o) + row * D + d4 * 4;
+    if constexpr (F32) {
+      *reinterpret_cast<float4*>(dst) = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+    } else {
+      uint2 w;
+      w.x = bf16x2_rn(O.x * inv, O.y * inv);
+      w.y = bf16x2_rn(O.z * inv, O.w * inv);
+      *reinterpret_cast<uint2*>(dst) = w;
+    }
+    if (d4 == 0 && a.lse) a.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;
+  }
+  if (csize > 1) cluster_sync_all();                                         // no CTA leaves while it is read
+}
+
+// Chunks: the tensor-core attention over the staged rows [B, t_pad, Hkv, 128] of the whole
+// key list (cache_stage_q8_kernel), so every key tile is one box.
+struct Q8TcProblem : EsaTcProblem {
+  int64_t t_pad;
+  __device__ int32_t kv_row(int64_t t) const { return (int32_t)(((int64_t)b * t_pad + t) * hkv + g); }
+  __device__ int kv_box(int j, int* y, int* z) const {
+    *y = g;
+    *z = (int)((int64_t)b * t_pad + (int64_t)j * kTcKeys);
+    return 1;
+  }
+};
+
+}  // namespace esa

@@ -1,0 +1,361 @@
+// cache_q8.cuh - the 8-bit key/value cache: rows quantised as they are written, and read
+// back.
+//
+// A cache operand holds codes [B, n_cap, Hkv, D] (e4m3 or int8) and one fp32 scale for
+// each block of 2^bshift tokens and head, [B, ceil(n_cap / block), Hkv]; the value of a
+// code is code * scale. Writing rows into a block gives it
+//   s' = max(s of the rows already in the block, 2^E),
+//   E  = the smallest integer with  max |new x| <= qmax 2^E  (qmax 448 / 127; E >= -100),
+// stores the new rows as round(x / s') and, where s' > s, the older rows as
+// round(code s / s'). The scale is a power of two on purpose: x / s' and code * s' are then
+// exact in fp32 (and code * s' in bf16, whose 8 significant bits hold every code), so a
+// code is the correctly rounded one whatever the order of the arithmetic, reading a row
+// back rounds nothing, and a growing scale costs the older rows one rounding of a halving
+// (e4m3: none, above its subnormals). An e4m3 code keeps its 3 mantissa bits under any
+// scale; an int8 code gives up to one of its 7 bits for it.
+#pragma once
+#include "common.cuh"
+#include "keylist.cuh"
+
+namespace esa {
+
+constexpr int kQ8E4M3 = 0, kQ8Int8 = 1;
+constexpr int kQ8LeastExp = -100;          // scales stay normal, and so do their reciprocals
+
+// ------------------------------------------------------------------ codes <-> values --
+// two e4m3 codes (the low 16 bits of a register) as f16, exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return h;
+}
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
+  float2 f;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+// four codes of a word as fp32
+template <int FMT>
+__device__ __forceinline__ void q8_widen4(uint32_t w, float* f) {
+  if constexpr (FMT == kQ8E4M3) {
+    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)w));
+    const float2 b = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(w >> 16)));
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(w >> (8 * e));
+  }
+}
+// four values as codes: nearest, ties to even, clamped to +-qmax
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_narrow4(const float* f) {
+  if constexpr (FMT == kQ8E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = __float2int_rn(fminf(fmaxf(f[e], -127.f), 127.f));
+      w |= ((uint32_t)c & 0xffu) << (8 * e);
+    }
+    return w;
+  }
+}
+
+// The smallest power of two s >= 2^kQ8LeastExp with amax <= qmax * s, from the bits of a
+// finite amax >= 0. qmax is 1.75 * 2^8 (e4m3) or 1.984375 * 2^6 (int8): the exponent goes
+// up by one when amax's mantissa is above that of qmax.
+template <int FMT>
+__device__ __forceinline__ float q8_scale_of(uint32_t amax_bits) {
+  constexpr int top_exp = FMT == kQ8E4M3 ? 8 : 6;
+  constexpr uint32_t top_mant = FMT == kQ8E4M3 ? 0x600000u : 0x7e0000u;
+  int e = (int)(amax_bits >> 23) - 127 - top_exp + ((amax_bits & 0x7fffffu) > top_mant ? 1 : 0);
+  e = max(e, kQ8LeastExp);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// ------------------------------------------------------------------------- write --
+struct CacheWriteArgs {
+  const void* x[2];        // new keys, new values: row (b, r) at x + b * bs + r * rs, [Hkv, D] contiguous
+  int64_t bs[2], rs[2];    // elements
+  uint8_t* codes[2];       // [B, n_cap, Hkv, D]
+  float* scale[2];         // [B, nblk, Hkv]
+  int64_t n_cap, nblk;
+  int64_t start;           // first position (no device lengths)
+  int64_t rows;            // new rows of a sequence (the most, with new_len)
+  const int64_t* seq_len;  // null, or [B]: rows end at seq_len[b]
+  const int64_t* new_len;  // null, or [B]: new rows of sequence b
+  int hkv, bshift;
+};
+
+// Positions [start, end) that sequence b writes. False: nothing (an empty write, or
+// lengths that do not fit the cache: recorded, the sequence is left as it was).
+__device__ __forceinline__ bool q8_write_range(const CacheWriteArgs& a, int b, int64_t& start, int64_t& end) {
+  if (!a.seq_len) {
+    start = a.start;
+    end = a.start + a.rows;
+    return true;
+  }
+  const int64_t t = a.new_len ? a.new_len[b] : a.rows;
+  end = a.seq_len[b];
+  if (t == 0) return false;
+  if (t < 0 || t > a.rows || end < t || end > a.n_cap) {
+    if (threadIdx.x == 0) record_status(1u, 705);
+    return false;
+  }
+  start = end - t;
+  return true;
+}
+
+// One CTA per (block of tokens, head, operand) of a sequence: block * D / 64 threads, so
+// that a thread holds 8 elements of each of 8 rows in registers and the block is read
+// once: load everything, take the maximum, scale, round, store. Bound by HBM (and by
+// launch and one memory latency for a single token). grid (blocks * 2 Hkv, B), heads
+// fastest: the CTAs that share rows run together, so DRAM pages are read whole.
+template <typename T, int D, int FMT>
+__global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArgs a) {
+  constexpr int TPR = D / 8;                       // threads of a row
+  constexpr int W = 8 * sizeof(T) / 4;             // 32-bit words of 8 elements: 4 or 8
+  constexpr int NP = 8;                            // rows of a thread
+  const uint32_t width = 2u * a.hkv, yb = blockIdx.x / width, col = blockIdx.x - yb * width;
+  const int op = col >= (uint32_t)a.hkv, h = col - (op ? a.hkv : 0), b = blockIdx.y;
+  int64_t start, end;
+  if (!q8_write_range(a, b, start, end)) return;
+  const int64_t blk = (start >> a.bshift) + yb;
+  const int64_t base = blk << a.bshift;
+  if (base >= end) return;
+  const int block = 1 << a.bshift;
+  const int row0 = threadIdx.x / TPR, piece = threadIdx.x % TPR, rpp = blockDim.x / TPR;
+  const T* src = static_cast<const T*>(op ? a.x[1] : a.x[0]) + (int64_t)b * a.bs[op] + (int64_t)h * D + piece * 8;
+  const int64_t rs = a.rs[op];
+  float* sc = a.scale[op] + ((int64_t)b * a.nblk + blk) * a.hkv + h;
+  uint8_t* codes = a.codes[op] + ((int64_t)b * a.n_cap * a.hkv + h) * D;     // + position * Hkv * D
+  const int64_t cs = (int64_t)a.hkv * D;
+
+  uint32_t x[NP][W];
+  bool mine[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = row0 + p * rpp;
+    const int64_t pos = base + r;
+    mine[p] = r < block && pos >= start && pos < end;
+#pragma unroll
+    for (int q = 0; q < W / 4; ++q) {
+      const uint4 v = mine[p] ? ld_stream16(src + (pos - start) * rs + q * 4) : make_uint4(0u, 0u, 0u, 0u);
+      x[p][4 * q] = v.x; x[p][4 * q + 1] = v.y; x[p][4 * q + 2] = v.z; x[p][4 * q + 3] = v.w;
+    }
+  }
+  float old = start > base ? *sc : 0.f;            // rows before the write hold their values under it
+  old = old > 0.f && old < INFINITY ? old : 0.f;
+
+  // maximum magnitude as bits: of floats >= 0 the order of the bits is the order of the
+  // values, and infinities and NaN come out on top
+  auto block_max = [&](uint32_t mx) -> uint32_t {
+    __shared__ uint32_t part[8];
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (blockDim.x > 32) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mx;
+      __syncthreads();
+      for (int w = 0; w < (int)blockDim.x >> 5; ++w) mx = max(mx, part[w]);
+    }
+    return mx;
+  };
+  uint32_t mx = 0;
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if constexpr (sizeof(T) == 2) mx = __vmaxu2(mx, x[p][w] & 0x7fff7fffu);
+      else mx = max(mx, x[p][w] & 0x7fffffffu);
+    }
+  if constexpr (sizeof(T) == 2) mx = max(mx & 0xffff0000u, mx << 16);
+  mx = block_max(mx);
+  if (mx >= 0x7f800000u) {
+    // not finite: NaN becomes 0, an infinity the largest code of a block scaled by its
+    // finite values; recorded for the host
+    if (threadIdx.x == 0) record_status(7u, 705);
+    uint32_t fin = 0;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int e = 0; e < (sizeof(T) == 2 ? 2 : 1); ++e) {
+          const uint32_t v = sizeof(T) == 4 ? x[p][w] : (e ? x[p][w] & 0xffff0000u : x[p][w] << 16);
+          const uint32_t m = v & 0x7fffffffu;
+          if (m > 0x7f800000u) x[p][w] &= sizeof(T) == 4 ? 0u : (e ? 0x0000ffffu : 0xffff0000u);
+          else if (m < 0x7f800000u) fin = max(fin, m);
+        }
+    mx = block_max(fin);
+  }
+  const float s = fmaxf(q8_scale_of<FMT>(mx), old);
+  const float inv = 1.f / s;                       // exact: powers of two
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if (!mine[p]) continue;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 2)
+        f[e] = __uint_as_float((e & 1) ? x[p][e / 2] & 0xffff0000u : x[p][e / 2] << 16) * inv;
+      else
+        f[e] = __uint_as_float(x[p][e]) * inv;
+    }
+    uint2 w;
+    w.x = q8_narrow4<FMT>(f);
+    w.y = q8_narrow4<FMT>(f + 4);
+    *reinterpret_cast<uint2*>(codes + (base + row0 + p * rpp) * cs + piece * 8) = w;
+  }
+  if (start > base && s > old) {
+    // the block's scale grew: the rows already there move to it
+    const float ratio = old * inv;
+    const int n = (int)(start - base) * (D / 16);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      uint4* p = reinterpret_cast<uint4*>(codes + (base + i / (D / 16)) * cs) + i % (D / 16);
+      uint4 v = *p;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float f[4];
+        q8_widen4<FMT>(w[q], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] *= ratio;
+        w[q] = q8_narrow4<FMT>(f);
+      }
+      *p = v;
+    }
+  }
+  // every thread has read the old scale before block_max's barriers
+  if (blockDim.x <= 32) __syncwarp();
+  if (threadIdx.x == 0) *sc = s;
+}
+
+// -------------------------------------------------------------------------- read --
+// 32 bytes of values to global memory in one store
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// N = 32 / sizeof(T) codes at src times s as 32 bytes of T at dst
+template <typename T, int FMT>
+__device__ __forceinline__ void q8_widen_store(const uint32_t* c, float s, T* dst) {
+  constexpr int N = 32 / sizeof(T);
+  float f[N];
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) q8_widen4<FMT>(c[q], f + 4 * q);
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (sizeof(T) == 2) w[e] = bf16x2_rn(f[2 * e] * s, f[2 * e + 1] * s);
+    else w[e] = __float_as_uint(f[e] * s);
+  }
+  st_global_32(dst, w);
+}
+template <int BYTES>
+__device__ __forceinline__ void q8_load_codes(const uint8_t* p, uint32_t* c) {
+  if constexpr (BYTES == 16) {
+    const uint4 v = ld_stream16(p);
+    c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    c[0] = v.x; c[1] = v.y;
+  }
+}
+
+struct CacheReadArgs {
+  const uint8_t* codes[2];
+  const float* scale[2];
+  void* out[2];             // [B, n, Hkv, D]; null: not wanted
+  const int32_t* idx;       // null, or [B, n]
+  int64_t n_cap, nblk, start, n;
+  int hkv, d, bshift;
+};
+
+constexpr int kReadThreads = 256, kReadPer = 4;
+
+// Row (b, r) of the result is cache row start + r, or idx[b, r] (zeros where that is not a
+// row of the cache). A thread makes 32 bytes of the result from 16 (8) codes, kReadPer of
+// them with their loads in flight together. Bound by HBM. grid (pieces, B, operands).
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const CacheReadArgs a) {
+  constexpr int N = 32 / sizeof(T);
+  const int op = blockIdx.z, b = blockIdx.y;
+  T* out = static_cast<T*>(a.out[op]);
+  if (!out) return;
+  const int per_row = a.hkv * a.d / N;
+  const int64_t total = a.n * per_row;
+  const int64_t i0 = (int64_t)blockIdx.x * (kReadThreads * kReadPer) + threadIdx.x;
+  uint32_t c[kReadPer][N / 4];
+  float s[kReadPer];
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    const int64_t i = i0 + u * kReadThreads;
+    s[u] = 0.f;
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) c[u][q] = 0u;
+    if (i >= total) continue;
+    const int64_t r = total < ((int64_t)1 << 31) ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
+    const int w = (int)(i - r * per_row);
+    const int64_t pos = a.idx ? (int64_t)a.idx[(int64_t)b * a.n + r] : a.start + r;
+    if (pos < 0 || pos >= a.n_cap) continue;
+    q8_load_codes<N>(a.codes[op] + ((int64_t)b * a.n_cap + pos) * a.hkv * a.d + w * N, c[u]);
+    s[u] = __ldg(a.scale[op] + ((int64_t)b * a.nblk + (pos >> a.bshift)) * a.hkv + w * N / a.d);
+  }
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    const int64_t i = i0 + u * kReadThreads;
+    if (i < total) q8_widen_store<T, FMT>(c[u], s[u], out + ((int64_t)b * total + i) * N);
+  }
+}
+
+// The whole key list of a chunk (initial, selected, local and the chunk itself; one list
+// per sequence, or one per KV head) as bf16 rows [B, t_pad, Hkv, 128] for the tensor-core
+// attention; rows behind the list are zeros, up to t_pad (a multiple of the key tile).
+struct CacheStageArgs {
+  const uint8_t* codes[2];
+  const float* scale[2];
+  __nv_bfloat16* out[2];
+  KeyList keys;
+  int64_t n_cap, nblk, c0, t_pad;
+  int lq, hkv, lists, bshift;
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kReadThreads) cache_stage_q8_kernel(const CacheStageArgs a) {
+  const int op = blockIdx.z, b = blockIdx.y;
+  const int per_row = a.hkv * 8;                        // 16-code pieces of a token
+  const int64_t total = a.t_pad * per_row;
+  const int64_t i0 = (int64_t)blockIdx.x * (kReadThreads * kReadPer) + threadIdx.x;
+  uint32_t c[kReadPer][4];
+  float s[kReadPer];
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    const int64_t i = i0 + u * kReadThreads;
+    s[u] = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[u][q] = 0u;
+    if (i >= total) continue;
+    const int64_t t = total < ((int64_t)1 << 31) ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
+    const int w = (int)(i - t * per_row), g = w >> 3;
+    const int list = a.lists > 1 ? b * a.lists + g : b;
+    const int cnt = min(max(a.keys.count[list], 0), (int)a.keys.idx_stride);
+    if (t >= a.keys.ni + cnt + (a.c0 - a.keys.lo) + a.lq) continue;
+    const int64_t pos = a.keys.pos(list, cnt, t);
+    q8_load_codes<16>(a.codes[op] + ((int64_t)b * a.n_cap + pos) * a.hkv * 128 + w * 16, c[u]);
+    s[u] = __ldg(a.scale[op] + ((int64_t)b * a.nblk + (pos >> a.bshift)) * a.hkv + g);
+  }
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    const int64_t i = i0 + u * kReadThreads;
+    if (i < total) q8_widen_store<__nv_bfloat16, FMT>(c[u], s[u], a.out[op] + ((int64_t)b * total + i) * 16);
+  }
+}
+
+}  // namespace esa

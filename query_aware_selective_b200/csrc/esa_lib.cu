@@ -18,8 +18,10 @@
 #include "../../include/esa.h"
 #include "attn_decode.cuh"
 #include "attn_pp.cuh"
+#include "attn_q8.cuh"
 #include "attn_simt.cuh"
 #include "attn_tc.cuh"
+#include "cache_q8.cuh"
 #include "cca.cuh"
 #include "common.cuh"
 #include "compress.cuh"
@@ -405,6 +407,8 @@ esa_status_t esa_device_status(void* stream) {
   if (code == 5u) return fail(ESA_ERR_CUDA, "kernel site %u found its shared memory misaligned and stopped", site);
   if (code == 1u)
     return fail(ESA_ERR_INVALID_ARG, "kernel site %u read a sequence length outside [1, n_cap] (clamped)", site);
+  if (code == 7u)
+    return fail(ESA_ERR_INVALID_ARG, "kernel site %u wrote NaN or infinite values to an 8-bit cache", site);
   if (code == 6u)
     return fail(ESA_ERR_INVALID_ARG,
                 "site %u: a Cholesky pivot was not positive (the matrix is not positive definite; a ridge helps)",
@@ -1157,6 +1161,361 @@ esa_status_t sparse_attn_impl(const void* q, const void* k, const void* v, esa_d
 }
 
 }  // namespace
+
+// ------------------------------------------------------------- 8-bit key/value cache --
+namespace {
+
+esa_status_t check_cache_q8(const esa_cache_q8_t& c) {
+  if (c.batch <= 0 || c.hkv <= 0 || c.n_cap <= 0)
+    return fail(ESA_ERR_INVALID_ARG, "batch, hkv and n_cap of the cache must be >= 1");
+  if (c.head_dim != 64 && c.head_dim != 128) return fail(ESA_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", c.head_dim);
+  if (c.block != 16 && c.block != 32 && c.block != 64 && c.block != 128)
+    return fail(ESA_ERR_UNSUPPORTED, "block %d (16, 32, 64 or 128)", c.block);
+  if (c.format != ESA_Q8_E4M3 && c.format != ESA_Q8_INT8)
+    return fail(ESA_ERR_INVALID_ARG, "bad cache format %d", c.format);
+  if (c.n_cap >= ((int64_t)1 << 31)) return fail(ESA_ERR_UNSUPPORTED, "n_cap must be < 2^31");
+  if (c.batch > 65535 || c.hkv > 32767) return fail(ESA_ERR_UNSUPPORTED, "batch <= 65535 and hkv <= 32767");
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale) return fail(ESA_ERR_INVALID_ARG, "null pointer in the cache");
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4))
+    return fail(ESA_ERR_INVALID_ARG, "cache codes need 16-byte alignment, scales 4-byte");
+  return ESA_OK;
+}
+
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+template <typename T, int D>
+void launch_write_q8(const esa::CacheWriteArgs& a, int format, dim3 grid, int threads, cudaStream_t s) {
+  if (format == ESA_Q8_E4M3) esa::cache_write_q8_kernel<T, D, esa::kQ8E4M3><<<grid, threads, 0, s>>>(a);
+  else esa::cache_write_q8_kernel<T, D, esa::kQ8Int8><<<grid, threads, 0, s>>>(a);
+}
+
+esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int64_t rows, int64_t kbs, int64_t krs,
+                              int64_t vbs, int64_t vrs, const esa_cache_q8_t& c, int64_t start,
+                              const int64_t* seq_len, const int64_t* new_len, void* stream) {
+  const esa_status_t st = check_cache_q8(c);
+  if (st != ESA_OK) return st;
+  if (dt != ESA_F32 && dt != ESA_BF16) return fail(ESA_ERR_INVALID_ARG, "bad dtype %d", (int)dt);
+  if (rows < 0 || rows > c.n_cap) return fail(ESA_ERR_INVALID_ARG, "rows must be in [0, n_cap]");
+  if (!seq_len && (start < 0 || start > c.n_cap - rows))
+    return fail(ESA_ERR_INVALID_ARG, "need 0 <= start and start + rows <= n_cap");
+  if (rows == 0) return ok();
+  if (!k || !v) return fail(ESA_ERR_INVALID_ARG, "null pointer");
+  const int64_t width = (int64_t)c.hkv * c.head_dim, vec = dt == ESA_BF16 ? 8 : 4;
+  if (!aligned(k, 16) || !aligned(v, 16) || krs % vec || vrs % vec || kbs % vec || vbs % vec)
+    return fail(ESA_ERR_INVALID_ARG, "rows of k and v need 16-byte alignment");
+  if ((rows > 1 && (krs < width || vrs < width)) || (c.batch > 1 && (kbs < 0 || vbs < 0)))
+    return fail(ESA_ERR_INVALID_ARG, "row strides must be >= hkv * head_dim, batch strides >= 0");
+  esa::CacheWriteArgs a{};
+  a.x[0] = k;
+  a.x[1] = v;
+  a.bs[0] = kbs;
+  a.bs[1] = vbs;
+  a.rs[0] = krs;
+  a.rs[1] = vrs;
+  a.codes[0] = static_cast<uint8_t*>(c.k);
+  a.codes[1] = static_cast<uint8_t*>(c.v);
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v_scale;
+  a.n_cap = c.n_cap;
+  a.nblk = cdiv(c.n_cap, c.block);
+  a.start = start;
+  a.rows = rows;
+  a.seq_len = seq_len;
+  a.new_len = new_len;
+  a.hkv = c.hkv;
+  a.bshift = log2_of(c.block);
+  // blocks that rows consecutive tokens can touch (with device lengths: from any offset)
+  const int64_t blocks = seq_len ? (rows + c.block - 2) / c.block + 1
+                                 : (start + rows - 1) / c.block - start / c.block + 1;
+  const int threads = std::max(32, c.block * c.head_dim / 64);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (blocks * 2 * c.hkv >= ((int64_t)1 << 31)) return fail(ESA_ERR_UNSUPPORTED, "too many rows in one write");
+  const dim3 grid((unsigned)(blocks * 2 * c.hkv), c.batch);
+  if (dt == ESA_BF16) {
+    if (c.head_dim == 128) launch_write_q8<__nv_bfloat16, 128>(a, c.format, grid, threads, s);
+    else launch_write_q8<__nv_bfloat16, 64>(a, c.format, grid, threads, s);
+  } else {
+    if (c.head_dim == 128) launch_write_q8<float, 128>(a, c.format, grid, threads, s);
+    else launch_write_q8<float, 64>(a, c.format, grid, threads, s);
+  }
+  ESA_LAUNCH_CHECK("cache_write_q8_kernel");
+  return ok();
+}
+
+bool q8_tensor_cores(int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
+  const int g = hq / hkv;
+  return dt == ESA_BF16 && head_dim == 128 && (int64_t)lq * g >= 64 && (g == 1 || g == 2 || g == 4 || g == 8);
+}
+
+int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
+  const Regions r = regions(c0, p);
+  return cdiv(r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq, esa::kTcKeys) * esa::kTcKeys;
+}
+
+// How a few-query call is spread: hc KV heads per CTA (its 8 warps split each head's keys
+// 8 / hc ways) and clusters of csize CTAs per unit of work, aiming at two CTAs on each of
+// the 148 SMs with at least one step of keys per warp.
+struct Q8Plan {
+  int hc, csize;
+};
+Q8Plan plan_q8(int64_t batch, int64_t tiles, int hkv, int64_t n_keys) {
+  const int64_t slots = 2 * 148, steps = cdiv(n_keys, esa::kQ8Keys);
+  Q8Plan best{1, 1};
+  int64_t best_ctas = 0;
+  for (int hc = 8; hc >= 1; hc /= 2) {
+    if (hkv % hc) continue;
+    const int64_t units = batch * tiles * (hkv / hc), kw = esa::kQ8Warps / hc;
+    const int64_t c = std::max<int64_t>(1, std::min<int64_t>({8, slots / units, cdiv(steps, kw)}));
+    const int64_t ctas = std::min<int64_t>(units * c, slots);
+    if (ctas > best_ctas) {
+      best_ctas = ctas;
+      best = Q8Plan{hc, (int)c};
+    }
+  }
+  return best;
+}
+
+template <typename T, int D, int FMT, int NT>
+esa_status_t launch_attn_q8(const esa::AttnQ8Args& a, dim3 grid, int csize, cudaStream_t s) {
+  constexpr int smem = esa::q8_smem_bytes<NT, D>();
+  static const char what = 0;
+  const esa_status_t st =
+      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_kernel<T, D, FMT, NT>, smem); });
+  if (st != ESA_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(esa::kQ8Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = csize;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  ESA_CUDA(cudaLaunchKernelEx(&cfg, esa::attn_q8_kernel<T, D, FMT, NT>, a));
+  ESA_LAUNCH_CHECK("attn_q8_kernel");
+  return ok();
+}
+template <typename T, int D>
+esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int nt, dim3 grid, int csize, cudaStream_t s) {
+  if (format == ESA_Q8_E4M3)
+    return nt == 1 ? launch_attn_q8<T, D, esa::kQ8E4M3, 1>(a, grid, csize, s)
+                   : launch_attn_q8<T, D, esa::kQ8E4M3, 2>(a, grid, csize, s);
+  return nt == 1 ? launch_attn_q8<T, D, esa::kQ8Int8, 1>(a, grid, csize, s)
+                 : launch_attn_q8<T, D, esa::kQ8Int8, 2>(a, grid, csize, s);
+}
+
+// The chunk form: the key list dequantised into the workspace, then attn_tc_kernel.
+esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, int64_t c0, int32_t hq,
+                           const esa::KeyList& keys, int lists, const esa_params_t& p, float sl2, void* o, float* lse,
+                           void* workspace, cudaStream_t s) {
+  const int g = hq / c.hkv;
+  const int64_t t_pad = q8_staged_rows(lq, c0, p);
+  if (c.batch * t_pad * c.hkv >= ((int64_t)1 << 31) || (int64_t)c.batch * lq * hq >= ((int64_t)1 << 31))
+    return fail(ESA_ERR_UNSUPPORTED, "more than 2^31 K/V or Q rows");
+  static const char what = 0;
+  esa_status_t st =
+      once_per_context(&what, [] { return set_max_smem(esa::attn_tc_kernel<esa::Q8TcProblem>, esa::kTcSmemBytes); });
+  if (st != ESA_OK) return st;
+  uint8_t* ks = static_cast<uint8_t*>(workspace);
+  uint8_t* vs = ks + up256((size_t)c.batch * t_pad * c.hkv * c.head_dim * 2);
+  CUtensorMap bq, bk, bv;
+  if ((st = make_tmap_box_bf16(&bq, q, hq, (uint64_t)c.batch * lq, g, esa::kTcRows / g)) != ESA_OK) return st;
+  if ((st = make_tmap_box_bf16(&bk, ks, c.hkv, (uint64_t)c.batch * t_pad, 1, esa::kTcKeys)) != ESA_OK) return st;
+  if ((st = make_tmap_box_bf16(&bv, vs, c.hkv, (uint64_t)c.batch * t_pad, 1, esa::kTcKeys)) != ESA_OK) return st;
+  esa::CacheStageArgs a{};
+  a.codes[0] = static_cast<const uint8_t*>(c.k);
+  a.codes[1] = static_cast<const uint8_t*>(c.v);
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v_scale;
+  a.out[0] = reinterpret_cast<__nv_bfloat16*>(ks);
+  a.out[1] = reinterpret_cast<__nv_bfloat16*>(vs);
+  a.keys = keys;
+  a.n_cap = c.n_cap;
+  a.nblk = cdiv(c.n_cap, c.block);
+  a.c0 = c0;
+  a.t_pad = t_pad;
+  a.lq = lq;
+  a.hkv = c.hkv;
+  a.lists = lists;
+  a.bshift = log2_of(c.block);
+  const dim3 sgrid((unsigned)cdiv(t_pad * c.hkv * 8, esa::kReadThreads * esa::kReadPer), c.batch, 2);
+  if (c.format == ESA_Q8_E4M3) esa::cache_stage_q8_kernel<esa::kQ8E4M3><<<sgrid, esa::kReadThreads, 0, s>>>(a);
+  else esa::cache_stage_q8_kernel<esa::kQ8Int8><<<sgrid, esa::kReadThreads, 0, s>>>(a);
+  ESA_LAUNCH_CHECK("cache_stage_q8_kernel");
+  esa::Q8TcProblem pr{};
+  pr.q = static_cast<const __nv_bfloat16*>(q);
+  pr.o = static_cast<__nv_bfloat16*>(o);
+  pr.lse = lse;
+  pr.keys = keys;
+  pr.n_cap = c.n_cap;
+  pr.c0 = c0;
+  pr.lq = lq;
+  pr.hq = hq;
+  pr.hkv = c.hkv;
+  pr.G = g;
+  pr.sl2 = sl2;
+  pr.lists = lists;
+  pr.t_pad = t_pad;
+  const dim3 grid((unsigned)cdiv((int64_t)lq * g, esa::kTcRows), c.hkv, c.batch);
+  // every tile is a box, so the row-gather maps are never read: the box maps stand in
+  esa::attn_tc_kernel<esa::Q8TcProblem><<<grid, esa::kTcThreads, esa::kTcSmemBytes, s>>>(bq, bk, bv, bq, bk, bv, bk,
+                                                                                        bv, pr);
+  ESA_LAUNCH_CHECK("attn_tc_kernel<q8>");
+  return ok();
+}
+
+esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_q8_t& c, int32_t lq, int64_t c0,
+                                 const int64_t* seq_len, int32_t hq, const int32_t* idx, const int32_t* count,
+                                 int32_t lists, const esa_params_t& p, float scale, void* o, float* lse,
+                                 void* workspace, size_t ws_bytes, void* stream) {
+  esa_status_t st = check_params(p);
+  if (st != ESA_OK) return st;
+  if ((st = check_cache_q8(c)) != ESA_OK) return st;
+  if (dt != ESA_F32 && dt != ESA_BF16) return fail(ESA_ERR_INVALID_ARG, "bad dtype %d", (int)dt);
+  if (lq <= 0) return fail(ESA_ERR_INVALID_ARG, "lq must be >= 1");
+  if (hq <= 0 || hq % c.hkv) return fail(ESA_ERR_INVALID_ARG, "hq must be a positive multiple of hkv");
+  if (lists != 1 && lists != c.hkv) return fail(ESA_ERR_INVALID_ARG, "lists must be 1 or hkv (got %d)", lists);
+  if (c0 < 0 || c0 > c.n_cap - lq) return fail(ESA_ERR_INVALID_ARG, "need 0 <= c0 and c0 + lq <= n_cap");
+  if (!q || !o || !idx || !count) return fail(ESA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q, 16) || !aligned(o, 16)) return fail(ESA_ERR_INVALID_ARG, "q and o need 16-byte alignment");
+  if (std::isnan(scale)) return fail(ESA_ERR_INVALID_ARG, "scale is NaN");
+  if (scale <= 0.f) scale = 1.f / std::sqrt((float)c.head_dim);
+  const float sl2 = scale * 1.4426950408889634f;
+  const Regions r = regions(c0, p);
+  // positions in a key list are 32-bit (counts are clamped to topk on the device)
+  if (r.ni + (int64_t)p.topk + (c0 - r.lo) + lq >= ((int64_t)1 << 31) - 64)
+    return fail(ESA_ERR_UNSUPPORTED, "a key list of 2^31 tokens or more");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  esa::KeyList keys{idx, p.topk, r.ni, r.lo, c.n_cap, count};
+  if (seq_len) keys.vl = esa::VarLen{seq_len, c.n_cap, p.n_init, p.window, 1};
+  else if (q8_tensor_cores(lq, hq, c.hkv, c.head_dim, dt)) {
+    const size_t need = esa_sparse_attn_q8_workspace_size(c.batch, lq, c0, hq, c.hkv, c.head_dim, dt, p);
+    if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+      return fail(ESA_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+    return attn_q8_chunk(q, c, lq, c0, hq, keys, lists, p, sl2, o, lse, workspace, s);
+  }
+  const int g = hq / c.hkv;
+  const int64_t rows = (int64_t)lq * g;
+  const int nt = rows <= 8 ? 1 : 2;
+  const int64_t tiles = cdiv(rows, 8 * nt);
+  const Q8Plan pl = plan_q8(c.batch, tiles, c.hkv, r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq);
+  if (tiles * (c.hkv / pl.hc) > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
+  esa::AttnQ8Args a{};
+  a.q = q;
+  a.k = static_cast<const uint8_t*>(c.k);
+  a.v = static_cast<const uint8_t*>(c.v);
+  a.ks = c.k_scale;
+  a.vs = c.v_scale;
+  a.o = o;
+  a.lse = lse;
+  a.keys = keys;
+  a.n_cap = c.n_cap;
+  a.nblk = cdiv(c.n_cap, c.block);
+  a.c0 = c0;
+  a.lq = lq;
+  a.hq = hq;
+  a.hkv = c.hkv;
+  a.G = g;
+  a.lists = lists;
+  a.bshift = log2_of(c.block);
+  a.hc = pl.hc;
+  a.tiles = (int)tiles;
+  a.scale_log2 = sl2;
+  const dim3 grid((unsigned)pl.csize, (unsigned)(tiles * (c.hkv / pl.hc)), c.batch);
+  if (dt == ESA_BF16)
+    return c.head_dim == 128 ? dispatch_attn_q8<__nv_bfloat16, 128>(a, c.format, nt, grid, pl.csize, s)
+                             : dispatch_attn_q8<__nv_bfloat16, 64>(a, c.format, nt, grid, pl.csize, s);
+  return c.head_dim == 128 ? dispatch_attn_q8<float, 128>(a, c.format, nt, grid, pl.csize, s)
+                           : dispatch_attn_q8<float, 64>(a, c.format, nt, grid, pl.csize, s);
+}
+
+}  // namespace
+
+esa_status_t esa_cache_write_q8(const void* k, const void* v, esa_dtype_t dt, int64_t rows, int64_t k_batch_stride,
+                                int64_t k_row_stride, int64_t v_batch_stride, int64_t v_row_stride,
+                                esa_cache_q8_t cache, int64_t start, void* stream) {
+  return cache_write_impl(k, v, dt, rows, k_batch_stride, k_row_stride, v_batch_stride, v_row_stride, cache, start,
+                          nullptr, nullptr, stream);
+}
+
+esa_status_t esa_cache_write_q8_varlen(const void* k, const void* v, esa_dtype_t dt, int64_t rows,
+                                       int64_t k_batch_stride, int64_t k_row_stride, int64_t v_batch_stride,
+                                       int64_t v_row_stride, esa_cache_q8_t cache, const int64_t* seq_len,
+                                       const int64_t* new_len, void* stream) {
+  if (!seq_len) return fail(ESA_ERR_INVALID_ARG, "null pointer");
+  return cache_write_impl(k, v, dt, rows, k_batch_stride, k_row_stride, v_batch_stride, v_row_stride, cache, 0,
+                          seq_len, new_len, stream);
+}
+
+esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows, const int32_t* idx, void* k_out,
+                               void* v_out, esa_dtype_t dt, void* stream) {
+  const esa_status_t st = check_cache_q8(cache);
+  if (st != ESA_OK) return st;
+  if (dt != ESA_F32 && dt != ESA_BF16) return fail(ESA_ERR_INVALID_ARG, "bad dtype %d", (int)dt);
+  if (rows < 0) return fail(ESA_ERR_INVALID_ARG, "rows must be >= 0");
+  if (!idx && (start < 0 || start > cache.n_cap - rows))
+    return fail(ESA_ERR_INVALID_ARG, "need 0 <= start and start + rows <= n_cap");
+  if (rows == 0 || (!k_out && !v_out)) return ok();
+  if (!aligned(k_out, 32) || !aligned(v_out, 32)) return fail(ESA_ERR_INVALID_ARG, "outputs need 32-byte alignment");
+  esa::CacheReadArgs a{};
+  a.codes[0] = static_cast<const uint8_t*>(cache.k);
+  a.codes[1] = static_cast<const uint8_t*>(cache.v);
+  a.scale[0] = cache.k_scale;
+  a.scale[1] = cache.v_scale;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.idx = idx;
+  a.n_cap = cache.n_cap;
+  a.nblk = cdiv(cache.n_cap, cache.block);
+  a.start = start;
+  a.n = rows;
+  a.hkv = cache.hkv;
+  a.d = cache.head_dim;
+  a.bshift = log2_of(cache.block);
+  const int64_t codes = dt == ESA_BF16 ? 16 : 8;            // of a thread's 32-byte store
+  const int64_t ctas = cdiv(rows * (cache.hkv * cache.head_dim / codes), esa::kReadThreads * esa::kReadPer);
+  if (ctas >= ((int64_t)1 << 31)) return fail(ESA_ERR_UNSUPPORTED, "too many rows in one read");
+  const dim3 grid((unsigned)ctas, cache.batch, 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache.format == ESA_Q8_E4M3) {
+    if (dt == ESA_BF16) esa::cache_read_q8_kernel<__nv_bfloat16, esa::kQ8E4M3><<<grid, esa::kReadThreads, 0, s>>>(a);
+    else esa::cache_read_q8_kernel<float, esa::kQ8E4M3><<<grid, esa::kReadThreads, 0, s>>>(a);
+  } else {
+    if (dt == ESA_BF16) esa::cache_read_q8_kernel<__nv_bfloat16, esa::kQ8Int8><<<grid, esa::kReadThreads, 0, s>>>(a);
+    else esa::cache_read_q8_kernel<float, esa::kQ8Int8><<<grid, esa::kReadThreads, 0, s>>>(a);
+  }
+  ESA_LAUNCH_CHECK("cache_read_q8_kernel");
+  return ok();
+}
+
+size_t esa_sparse_attn_q8_workspace_size(int32_t batch, int32_t lq, int64_t c0, int32_t hq, int32_t hkv,
+                                         int32_t head_dim, esa_dtype_t dt, esa_params_t p) {
+  if (batch <= 0 || lq <= 0 || c0 < 0 || hkv <= 0 || hq <= 0 || hq % hkv) return 0;
+  if (!q8_tensor_cores(lq, hq, hkv, head_dim, dt)) return 0;
+  return 2 * up256((size_t)batch * q8_staged_rows(lq, c0, p) * hkv * head_dim * 2);
+}
+
+esa_status_t esa_sparse_attn_q8(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, int32_t lq, int64_t c0,
+                                int32_t hq, const int32_t* idx, const int32_t* count, int32_t lists, esa_params_t p,
+                                float scale, void* o, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return sparse_attn_q8_impl(q, dt, cache, lq, c0, nullptr, hq, idx, count, lists, p, scale, o, lse, workspace,
+                             ws_bytes, stream);
+}
+
+esa_status_t esa_sparse_attn_q8_varlen(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, const int64_t* seq_len,
+                                       int32_t hq, const int32_t* idx, const int32_t* count, int32_t lists,
+                                       esa_params_t p, float scale, void* o, float* lse, void* stream) {
+  if (!seq_len) return fail(ESA_ERR_INVALID_ARG, "null pointer");
+  return sparse_attn_q8_impl(q, dt, cache, 1, cache.n_cap - 1, seq_len, hq, idx, count, lists, p, scale, o, lse,
+                             nullptr, 0, stream);
+}
 
 // ------------------------------------------------------------------ MoBA --
 namespace {

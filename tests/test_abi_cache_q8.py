@@ -1,0 +1,133 @@
+"""Host-side checks of the 8-bit cache calls that need no GPU: every bad argument is
+refused before anything is launched, by the C ABI and by the binding."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import query_aware_selective_b200 as qas
+from query_aware_selective_b200 import _abi
+from query_aware_selective_b200 import build as qbuild
+
+FAKE = 0x10000      # 256-byte aligned, never dereferenced on the refused paths
+INVALID, UNSUPPORTED, WORKSPACE = _abi.ESA_ERR_INVALID_ARG, _abi.ESA_ERR_UNSUPPORTED, _abi.ESA_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module")
+def lib():
+    qbuild.build()
+    return _abi.load()
+
+
+def cache(k=FAKE, ks=FAKE, v=FAKE, vs=FAKE, n_cap=4096, batch=2, hkv=8, d=128, block=64, fmt=0):
+    return _abi.EsaCacheQ8(k, ks, v, vs, n_cap, batch, hkv, d, block, fmt)
+
+
+BAD_CACHES = [(dict(k=None), INVALID), (dict(ks=None), INVALID), (dict(v=None), INVALID), (dict(vs=None), INVALID),
+              (dict(k=FAKE + 8), INVALID), (dict(v=FAKE + 1), INVALID), (dict(ks=FAKE + 2), INVALID),
+              (dict(n_cap=0), INVALID), (dict(n_cap=1 << 31), UNSUPPORTED), (dict(batch=0), INVALID),
+              (dict(batch=65536), UNSUPPORTED), (dict(hkv=0), INVALID), (dict(d=96), UNSUPPORTED),
+              (dict(block=48), UNSUPPORTED), (dict(block=256), UNSUPPORTED), (dict(block=0), UNSUPPORTED),
+              (dict(fmt=2), INVALID)]
+
+
+def test_struct_layout():
+    assert ctypes.sizeof(_abi.EsaCacheQ8) == 4 * 8 + 8 + 5 * 4 + 4
+    assert [f[0] for f in _abi.EsaCacheQ8._fields_] == ["k", "k_scale", "v", "v_scale", "n_cap", "batch", "hkv",
+                                                        "head_dim", "block", "format"]
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_bad_caches_are_refused_by_every_call(lib, bad, status):
+    before = lib.esa_launch_count()
+    c = cache(**bad)
+    p = _abi.params(128, 512, 256, 2)
+    assert lib.esa_cache_write_q8(FAKE, FAKE, 1, 8, 8192, 1024, 8192, 1024, c, 0, None) == status
+    assert lib.esa_cache_write_q8_varlen(FAKE, FAKE, 1, 1, 1024, 1024, 1024, 1024, c, FAKE, None, None) == status
+    assert lib.esa_cache_read_q8(c, 0, 8, None, FAKE, FAKE, 1, None) == status
+    hq = 4 * max(1, c.hkv)
+    assert lib.esa_sparse_attn_q8(FAKE, 1, c, 1, 1000, hq, FAKE, FAKE, 1, p, 0.0, FAKE, None, FAKE, 1 << 40,
+                                  None) == status
+    assert lib.esa_sparse_attn_q8_varlen(FAKE, 1, c, FAKE, hq, FAKE, FAKE, 1, p, 0.0, FAKE, None, None) == status
+    assert lib.esa_launch_count() == before
+
+
+def test_write_refusals(lib):
+    before = lib.esa_launch_count()
+
+    def w(k=FAKE, v=FAKE, dt=1, rows=8, kb=8192, kr=1024, vb=8192, vr=1024, start=0, **c):
+        return lib.esa_cache_write_q8(k, v, dt, rows, kb, kr, vb, vr, cache(**c), start, None)
+    assert w(k=None) == INVALID and w(v=None) == INVALID
+    assert w(dt=2) == INVALID
+    assert w(rows=-1) == INVALID and w(rows=4097) == INVALID
+    assert w(start=-1) == INVALID and w(start=4089) == INVALID and w(start=2 ** 62) == INVALID
+    assert w(k=FAKE + 8) == INVALID and w(v=FAKE + 8) == INVALID              # misaligned base
+    assert w(kr=1028) == INVALID and w(vb=8196) == INVALID                    # misaligned rows
+    assert w(dt=0, kr=1026) == INVALID
+    assert w(kr=512) == INVALID and w(vr=0) == INVALID                        # rows would overlap
+    assert w(kb=-8192) == INVALID
+    assert w(rows=0, k=None) == _abi.ESA_OK                                   # nothing to write
+    f = lib.esa_cache_write_q8_varlen
+    assert f(FAKE, FAKE, 1, 1, 1024, 1024, 1024, 1024, cache(), None, None, None) == INVALID
+    assert lib.esa_launch_count() == before
+
+
+def test_read_refusals(lib):
+    before = lib.esa_launch_count()
+
+    def r(start=0, rows=8, idx=None, k=FAKE, v=FAKE, dt=1):
+        return lib.esa_cache_read_q8(cache(), start, rows, idx, k, v, dt, None)
+    assert r(start=-1) == INVALID and r(start=4089) == INVALID and r(rows=-1) == INVALID
+    assert r(rows=2 ** 62) == INVALID
+    assert r(k=FAKE + 16) == INVALID and r(v=FAKE + 8) == INVALID
+    assert r(dt=3) == INVALID
+    assert r(rows=0) == _abi.ESA_OK and r(k=None, v=None) == _abi.ESA_OK
+    assert lib.esa_launch_count() == before
+
+
+def test_attention_refusals(lib):
+    before = lib.esa_launch_count()
+    good = _abi.params(128, 512, 256, 2)
+
+    def a(q=FAKE, dt=1, lq=1, c0=1000, hq=32, idx=FAKE, count=FAKE, lists=1, p=good, scale=0.0, o=FAKE, ws=FAKE,
+          nb=1 << 40, **c):
+        return lib.esa_sparse_attn_q8(q, dt, cache(**c), lq, c0, hq, idx, count, lists, p, scale, o, None, ws, nb, None)
+    assert a(q=None) == INVALID and a(o=None) == INVALID and a(idx=None) == INVALID and a(count=None) == INVALID
+    assert a(q=FAKE + 8) == INVALID and a(o=FAKE + 8) == INVALID
+    assert a(dt=2) == INVALID and a(lq=0) == INVALID
+    assert a(c0=-1) == INVALID and a(c0=4096) == INVALID and a(lq=5, c0=4092) == INVALID
+    assert a(hq=0) == INVALID and a(hq=30) == INVALID
+    assert a(lists=2) == INVALID and a(lists=0) == INVALID
+    assert a(scale=math.nan) == INVALID
+    assert a(p=_abi.params(128, 512, 0, 2)) == INVALID and a(p=_abi.params(-1, 512, 4, 2)) == INVALID
+    assert a(p=_abi.params(128, 512, 2 ** 31 - 1, 2)) == UNSUPPORTED
+    assert a(lq=64, ws=None) == WORKSPACE and a(lq=64, nb=1024) == WORKSPACE and a(lq=64, ws=FAKE + 64) == WORKSPACE
+    assert a(lq=4000, c0=0, hq=8 * 300, n_cap=4096, d=64) == UNSUPPORTED     # 75000 row tiles of 16
+    f = lib.esa_sparse_attn_q8_varlen
+    assert f(FAKE, 1, cache(), None, 32, FAKE, FAKE, 1, good, 0.0, FAKE, None, None) == INVALID
+    assert f(FAKE, 1, cache(), FAKE, 32, FAKE, FAKE, 3, good, 0.0, FAKE, None, None) == INVALID
+    assert lib.esa_launch_count() == before
+
+
+def test_workspace_is_for_chunks_only(lib):
+    p = _abi.params(128, 4096, 2048, 2)
+    size = _abi.sparse_attn_q8_workspace_size
+    assert size(16, 1, 131071, 32, 8, 128, 1, p) == 0                         # decode
+    assert size(1, 15, 32000, 32, 8, 128, 1, p) == 0                          # 60 rows
+    assert size(1, 64, 32000, 40, 8, 128, 1, p) == 0                          # groups of 5
+    assert size(1, 512, 32000, 32, 8, 128, 0, p) == 0                         # fp32
+    assert size(1, 512, 32000, 32, 8, 64, 1, p) == 0                          # head_dim 64
+    rows = 128 + 2048 + 4096 + 512                                            # 6784 = 53 * 128
+    assert size(1, 512, 32000, 32, 8, 128, 1, p) == 2 * rows * 8 * 128 * 2
+    assert size(1, 512, 0, 32, 8, 128, 1, p) == 2 * 512 * 8 * 128 * 2
+    assert size(0, 512, 0, 32, 8, 128, 1, p) == 0
+
+
+def test_binding_refuses_cpu_tensors():
+    k = torch.zeros((1, 64, 2, 64), dtype=torch.int8)
+    s = torch.zeros((1, 4, 2))
+    with pytest.raises(ValueError, match="CUDA"):
+        qas.CacheQ8(k, s, k.clone(), s.clone(), 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        qas.cache_q8(1, 64, 2, 64, device="cpu")
