@@ -506,14 +506,23 @@ def cache_q8(batch: int, n_cap: int, hkv: int, head_dim: int, dtype: torch.dtype
 def _q8_call(cache: CacheQ8, where: str, *args):
     """Call `where` with args and the current stream of the cache's device, under that
     device."""
-    dev = cache._k.device
+    dev = cache._k.device.index
     fn = getattr(load(), where)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if torch.cuda.current_device() == dev:
+        # the handle alone: torch.cuda.current_stream() builds a Stream object (3 us)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(st, where)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != ESA_OK:
+        _check(st, where)
+
+
+def _q8_empty(shape, dtype, device) -> torch.Tensor:
+    """torch.empty of a shape of 3 or 4 (empty_strided takes half its host time)."""
+    strides = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else \
+        (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _q8_tensor(t: torch.Tensor, name: str, cache: CacheQ8, dtype, shape):
@@ -585,7 +594,7 @@ def cache_read_q8(cache: CacheQ8, start: int = 0, rows: Optional[int] = None, id
         if not want:
             out = None
         elif out is None:
-            out = torch.empty(shape, dtype=dtype, device=cache._k.device)
+            out = _q8_empty(shape, dtype, cache._k.device)
         else:
             _q8_tensor(out, name, cache, dtype, shape)
         got.append(out)
@@ -615,7 +624,7 @@ def _q8_attn_args(q, cache: CacheQ8, idx, count, p: EsaParams, want_lse, out, ls
     if not want_lse:
         lse = None
     elif lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = _q8_empty(q.shape[:3], torch.float32, q.device)
     else:
         _q8_tensor(lse, "lse", cache, torch.float32, q.shape[:3])
     return lists, out, lse
@@ -633,8 +642,12 @@ def sparse_attn_q8(q: torch.Tensor, cache: CacheQ8, c0: int, idx: torch.Tensor, 
     [B, L] with L = 1 or Hkv (a list per KV head). Returns (o like q, lse [B, Lq, Hq] or None)."""
     lists, out, lse = _q8_attn_args(q, cache, idx, count, p, want_lse, out, lse)
     c, (b, lq, hq, d), dt = cache._c, q.shape, _dtype_code(q)
-    ws = _workspace(sparse_attn_q8_workspace_size(b, lq, c0, hq, c.hkv, d, dt, p), q.device, workspace)
-    wp, wn = _ws_ptr(ws)
+    wp, wn = None, 0
+    if lq > 1:                 # a single query needs no workspace
+        if workspace is not None and workspace.device != q.device:
+            raise ValueError("the workspace must be on the cache's device")
+        ws = _workspace(sparse_attn_q8_workspace_size(b, lq, c0, hq, c.hkv, d, dt, p), q.device, workspace)
+        wp, wn = _ws_ptr(ws)
     _q8_call(cache, "esa_sparse_attn_q8", _ptr(q), dt, c, lq, c0, hq, _ptr(idx), _ptr(count), lists, p, scale,
              _ptr(out), _ptr(lse), wp, wn)
     return out, lse

@@ -36,6 +36,7 @@ namespace esa {
 
 constexpr int kQ8Warps = 8, kQ8Threads = kQ8Warps * 32;
 constexpr int kQ8Keys = 16;                     // keys of a warp's step
+constexpr int kQ8Stages = 3;                    // steps of a warp's ring
 constexpr float kQ8Head = 10.f, kQ8Lazy = 5.f;  // weights reach 2^(10 + 5), below f16's 2^16
 
 struct AttnQ8Args {
@@ -57,10 +58,47 @@ struct AttnQ8Args {
 
 template <int NT, int D>
 __host__ __device__ constexpr int q8_row_floats() { return D + 4; }     // o, then padding
+// A step in a warp's ring: 16 key rows, 16 value rows, their 32 scales.
+template <int D>
+__host__ __device__ constexpr int q8_stage_bytes() { return 2 * kQ8Keys * D + 128; }
 template <int NT, int D>
 __host__ __device__ constexpr int q8_smem_bytes() {
-  // the warps' partial rows; (m, l) of every warp row; (m, l) of every merged row
-  return (kQ8Warps * 8 * NT * q8_row_floats<NT, D>() + 4 * kQ8Warps * 8 * NT) * 4;
+  // the rings; after the loop the warps' partial rows, (m, l) of every warp row, (m, l) of
+  // every merged row
+  constexpr int rings = kQ8Warps * kQ8Stages * q8_stage_bytes<D>();
+  constexpr int merge = (kQ8Warps * 8 * NT * q8_row_floats<NT, D>() + 4 * kQ8Warps * 8 * NT) * 4;
+  return rings > merge ? rings : merge;
+}
+// Byte offset of 16-byte piece c of row r of a step's keys / values. The pieces are placed
+// so that the eight lanes of a shared-memory phase hit all 32 banks: keys are read as rows
+// (gid, all tig), values as pieces gid, gid + 1 of rows 2 tig.
+template <int D>
+__device__ __forceinline__ uint32_t q8_k_off(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ ((r & 1) << 2)) << 4);
+  else return r * 64 + (c << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t q8_v_off(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ (((r >> 1) & 3) << 1)) << 4);
+  else return (r ^ ((r >> 2) & 1)) * 64 + ((c ^ (r & 2)) << 4);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -148,7 +186,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   constexpr int KC = D / 64;             // 16-byte pieces of a key row a lane takes (K)
   constexpr int VW = D / 32;             // words of a value row a lane takes (V)
   constexpr int RF = q8_row_floats<NT, D>();
-  extern __shared__ __align__(16) float q8sm[];
+  extern __shared__ __align__(128) float q8sm[];
   float* const sm_o = q8sm;                                    // [warp][ROWS][RF]
   float* const sm_ml = sm_o + kQ8Warps * ROWS * RF;            // [warp][ROWS][2]
   float* const sm_fin = sm_ml + 2 * kQ8Warps * ROWS;           // [head slot][ROWS][2]
@@ -218,10 +256,13 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     }
   }
 
-  // ---- the stream: positions two steps ahead, codes and scales one step ahead
+  // ---- the stream: the warp's own ring of kQ8Stages steps in shared memory, filled by
+  // 16-byte cp.async (8 or 4 lanes a row), positions looked up one step before that
+  constexpr int CPR = D / 16;                      // 16-byte pieces of a row
   const int64_t row_bytes = (int64_t)a.hkv * D;
-  const uint8_t* kb = a.k + (int64_t)b * a.n_cap * row_bytes + g * D + tig * 16;
-  const uint8_t* vb = a.v + (int64_t)b * a.n_cap * row_bytes + g * D + gid * (D / 8);
+  const int cpc = lane % CPR, cpr = lane / CPR;    // this lane's piece, and its row of each group of 32 / CPR
+  const uint8_t* kb = a.k + (int64_t)b * a.n_cap * row_bytes + g * D + cpc * 16;
+  const uint8_t* vb = a.v + (int64_t)b * a.n_cap * row_bytes + g * D + cpc * 16;
   const float* sb = (lane < 16 ? a.ks : a.vs) + (int64_t)b * a.nblk * a.hkv + g;
   const int32_t* ib = kl.idx + (int64_t)list * kl.idx_stride;
   const int ni = (int)kl.ni, jump = (int)(kl.lo - kl.ni) - cnt;
@@ -230,30 +271,17 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     int p = t < ni ? t : (t < ni + cnt ? __ldg(ib + t - ni) : t + jump);
     return min(max(p, 0), (int)a.n_cap - 1);
   };
-  uint4 kr[2][KC];
-  uint32_t vr[4][VW];
-  auto load_k = [&](int pos, uint4 (&k)[2][KC]) {
+  const uint32_t ring = smem_u32(q8sm) + warp * (kQ8Stages * q8_stage_bytes<D>());
+  auto issue = [&](int pos, uint32_t st) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t* p = kb + __shfl_sync(0xffffffffu, pos, gid + 8 * u) * row_bytes;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) k[u][c] = ld_stream16(p + c * 64);
+    for (int i = 0; i < kQ8Keys * CPR / 32; ++i) {
+      const int row = cpr + i * (32 / CPR);
+      const int64_t off = (int64_t)__shfl_sync(0xffffffffu, pos, row) * row_bytes;
+      cp_async16(st + q8_k_off<D>(row, cpc), kb + off, 16u);
+      cp_async16(st + kQ8Keys * D + q8_v_off<D>(row, cpc), vb + off, 16u);
     }
+    cp_async4(st + 2 * kQ8Keys * D + lane * 4, sb + (int64_t)(pos >> a.bshift) * a.hkv);
   };
-  auto load_v = [&](int pos, uint32_t (&v)[4][VW]) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint8_t* p = vb + __shfl_sync(0xffffffffu, pos, 2 * tig + (u & 1) + 8 * (u >> 1)) * row_bytes;
-      if constexpr (VW == 4) {
-        const uint4 x = ld_stream16(p);
-        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-      } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-        v[u][0] = x.x; v[u][1] = x.y;
-      }
-    }
-  };
-  auto load_s = [&](int pos) -> float { return __ldg(sb + (int64_t)(pos >> a.bshift) * a.hkv); };
 
   float acc[2 * VW][NT][4];              // O^T tiles: dims (2 t, 2 t + 1) of the lane's D / 8, rows 2 tig, 2 tig + 1
   float m[NT][2], l[NT][2];
@@ -271,23 +299,31 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][nt][e] = 0.f;
 
-  float sc = 1.f;
-  int pos_n = 0;
-  if (s_beg < s_end) {
-    const int pos = position(s_beg);
-    load_k(pos, kr);
-    load_v(pos, vr);
-    sc = load_s(pos);
-    if (s_beg + kw < s_end) pos_n = position(s_beg + kw);
-  }
-  for (int s = s_beg; s < s_end; s += kw) {
-    const bool more = s + kw < s_end;
-    const float sc_cur = sc;
-    uint4 kn[2][KC];
-    if (more) {
-      load_k(pos_n, kn);
-      sc = load_s(pos_n);
-    }
+  int pos_n = 0, s_n = s_beg;            // the next step to issue, and its positions
+  uint32_t st_n = ring;                  // and the ring slot it goes to
+  const uint32_t ring_end = ring + kQ8Stages * q8_stage_bytes<D>();
+  auto advance = [&](uint32_t st) { return st + q8_stage_bytes<D>() == ring_end ? ring : st + q8_stage_bytes<D>(); };
+  auto issue_next = [&]() {
+    if (s_n < s_end) issue(pos_n, st_n);
+    cp_async_commit();                   // one group per step, empty past the end
+    s_n += kw;
+    st_n = advance(st_n);
+    if (s_n < s_end) pos_n = position(s_n);
+  };
+  if (s_n < s_end) pos_n = position(s_n);
+#pragma unroll
+  for (int i = 0; i < kQ8Stages - 1; ++i) issue_next();
+  uint32_t st = ring;
+  for (int s = s_beg; s < s_end; s += kw, st = advance(st)) {
+    cp_async_wait<kQ8Stages - 2>();      // this lane's pieces of step s are here
+    __syncwarp();                        // every lane's are, and every lane has left the slot filled next
+    issue_next();
+    uint4 kr[2][KC];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < KC; ++c) kr[u][c] = lds128(st + q8_k_off<D>(gid + 8 * u, tig + 4 * c));
+    const float sc_cur = __uint_as_float(lds32(st + 2 * kQ8Keys * D + lane * 4));
 
     // S^T = Kc Q^T, two chains of half the dims
     float sx[NT][2][4];
@@ -384,6 +420,18 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     }
 
     // O^T += Vc^T W^T
+    uint32_t vr[4][VW];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = 2 * tig + (u & 1) + 8 * (u >> 1);
+      if constexpr (VW == 4) {
+        const uint4 x4 = lds128(st + kQ8Keys * D + q8_v_off<D>(row, gid));
+        vr[u][0] = x4.x; vr[u][1] = x4.y; vr[u][2] = x4.z; vr[u][3] = x4.w;
+      } else {
+        const uint2 x2 = lds64(st + kQ8Keys * D + q8_v_off<D>(row, gid >> 1) + (gid & 1) * 8);
+        vr[u][0] = x2.x; vr[u][1] = x2.y;
+      }
+    }
 #pragma unroll
     for (int w = 0; w < VW; ++w) {
       uint32_t da[4], db[4];
@@ -398,15 +446,9 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
             mma_f16(acc[2 * w + p][nt], da[2 * p], da[2 * p + 1], db[2 * p], db[2 * p + 1], wl[nt][0], wl[nt][1]);
         }
     }
-    if (more) {
-      load_v(pos_n, vr);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int c = 0; c < KC; ++c) kr[u][c] = kn[u][c];
-      if (s + 2 * kw < s_end) pos_n = position(s + 2 * kw);
-    }
   }
+  cp_async_wait_all();
+  __syncthreads();                       // the rings are free: the merge reuses them
 
   // ---- the warp's rows to shared memory
 #pragma unroll
