@@ -16,9 +16,9 @@
 // loop, only byte pairs of two keys brought side by side (prmt) and one conversion per
 // two codes. S^T becomes the B operand of the second product by movmatrix.
 // m is a reference, not the maximum: it is raised to max_j (x_j + log2 b_j) when that
-// exceeds it by 2^5, and W = 2^(.. - m + 10) <= 2^15 is rounded to f16 (relative 2^-11; a
-// weight under 2^-35 of the largest is lost, which 2^20 of them do not make visible). l
-// sums unrounded fp32 terms. fp32 queries go in as two f16 (q = hi + lo), and so do the
+// exceeds it by 5, and W = 2^(x_j + log2 b_j - m + 10) <= 2^15 is rounded to f16 (relative
+// 2^-11; a weight under 2^-35 of the largest is lost, which 2^20 of them do not make
+// visible). l sums the unrounded W 2^-10 / b_j. fp32 queries go in as two f16 (q = hi + lo), and so do the
 // weights, for 22 bits of each.
 //
 // Bound by HBM: each attended code is read once. A warp streams 16 keys a step, 16 bytes a
@@ -37,7 +37,7 @@ namespace esa {
 constexpr int kQ8Warps = 8, kQ8Threads = kQ8Warps * 32;
 constexpr int kQ8Keys = 16;                     // keys of a warp's step
 constexpr int kQ8Stages = 3;                    // steps of a warp's ring
-constexpr float kQ8Head = 10.f, kQ8Lazy = 5.f;  // weights reach 2^(10 + 5), below f16's 2^16
+constexpr float kQ8Head = 10.f, kQ8Most = 0x1p15f;  // weights: 2^10 at the reference, at most 2^15 (f16: 2^16)
 
 struct AttnQ8Args {
   const void* q;            // [B, Lq, Hq, D]
@@ -150,15 +150,6 @@ __device__ __forceinline__ void q8_transpose(uint32_t wa, uint32_t wb, uint32_t*
   }
 }
 
-// log2 of a positive scale; an integer, exactly, for a power of two. Scales under 2^-120
-// (zero among them) count as 2^-120.
-__device__ __forceinline__ float q8_log2(float s) {
-  const uint32_t u = __float_as_uint(fmaxf(s, 0x1p-120f));
-  const uint32_t mant = u & 0x7fffffu;
-  const float e = (float)((int)(u >> 23) - 127);
-  return mant ? e + __log2f(__uint_as_float(mant | 0x3f800000u)) : e;
-}
-
 // A power of two f (and its reciprocal's log2) that brings amax to [2^13, 2^14): queries
 // of any range fit f16, and the elements that matter stay normal there.
 __device__ __forceinline__ int q8_query_exp(float amax) {
@@ -212,6 +203,65 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   const int s_end = (int)((int64_t)steps * (rank + 1) / csize);
   const int s_beg = (int)((int64_t)steps * rank / csize) + kp;
 
+  // ---- the stream: the warp's own ring of kQ8Stages steps in shared memory, filled by
+  // 16-byte cp.async (8 or 4 lanes a row), positions looked up one step before that
+  constexpr int CPR = D / 16;                      // 16-byte pieces of a row
+  const uint32_t row_bytes = (uint32_t)a.hkv * D;
+  const int cpc = lane % CPR, cpr = lane / CPR;    // this lane's piece of a row, and which rows it copies
+  const uint8_t* kb = a.k + (int64_t)b * a.n_cap * row_bytes + g * D + cpc * 16;
+  const uint8_t* vb = a.v + (int64_t)b * a.n_cap * row_bytes + g * D + cpc * 16;
+  const float* sb = (lane < 16 ? a.ks : a.vs) + (int64_t)b * a.nblk * a.hkv + g;
+  const int32_t* ib = kl.idx + (int64_t)list * kl.idx_stride;
+  const int ni = (int)kl.ni, jump = (int)(kl.lo - kl.ni) - cnt;
+  auto position = [&](int s) -> int {              // of key slot lane % 16 of step s (a key behind the list: its last)
+    const int t = min(s * kQ8Keys + (lane & 15), n_keys - 1);
+    int p = t < ni ? t : (t < ni + cnt ? __ldg(ib + t - ni) : t + jump);
+    return min(max(p, 0), (int)a.n_cap - 1);
+  };
+  const uint32_t ring = smem_u32(q8sm) + warp * (kQ8Stages * q8_stage_bytes<D>());
+  auto issue = [&](int pos, uint32_t st) {
+#pragma unroll
+    for (int i = 0; i < kQ8Keys * CPR / 32; ++i) {
+      // rows whose bits that place a value's pieces (q8_v_off) are the same for every i
+      const int row = D == 128 ? 2 * cpr + (i & 1) + 8 * (i >> 1) : cpr + 8 * i;
+      const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, pos, row) * row_bytes;
+      cp_async16(st + q8_k_off<D>(row, cpc), kb + off, 16u);
+      cp_async16(st + kQ8Keys * D + q8_v_off<D>(row, cpc), vb + off, 16u);
+    }
+    cp_async4(st + 2 * kQ8Keys * D + lane * 4, sb + (int64_t)(pos >> a.bshift) * a.hkv);
+  };
+
+  float acc[2 * VW][NT][4];              // O^T tiles: dims (2 t, 2 t + 1) of the lane's D / 8, rows 2 tig, 2 tig + 1
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      m[nt][j] = -INFINITY;
+      l[nt][j] = 0.f;
+    }
+#pragma unroll
+  for (int t = 0; t < 2 * VW; ++t)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][nt][e] = 0.f;
+
+  int pos_n = 0, s_n = s_beg;            // the next step to issue, and its positions
+  uint32_t st_n = ring;                  // and the ring slot it goes to
+  const uint32_t ring_end = ring + kQ8Stages * q8_stage_bytes<D>();
+  auto advance = [&](uint32_t st) { return st + q8_stage_bytes<D>() == ring_end ? ring : st + q8_stage_bytes<D>(); };
+  auto issue_next = [&]() {
+    if (s_n < s_end) issue(pos_n, st_n);
+    cp_async_commit();                   // one group per step, empty past the end
+    s_n += kw;
+    st_n = advance(st_n);
+    if (s_n < s_end) pos_n = position(s_n);
+  };
+  if (s_n < s_end) pos_n = position(s_n);
+#pragma unroll
+  for (int i = 0; i < kQ8Stages - 1; ++i) issue_next();
+
   // ---- queries: B fragments, row gid of each group of 8, dims in the order of K's words
   uint32_t qf[NT][KC][4][2], ql[F32 ? NT : 1][KC][4][2];
   float xs[NT][2];                                             // logit factors of rows 2 tig, 2 tig + 1
@@ -256,63 +306,6 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     }
   }
 
-  // ---- the stream: the warp's own ring of kQ8Stages steps in shared memory, filled by
-  // 16-byte cp.async (8 or 4 lanes a row), positions looked up one step before that
-  constexpr int CPR = D / 16;                      // 16-byte pieces of a row
-  const int64_t row_bytes = (int64_t)a.hkv * D;
-  const int cpc = lane % CPR, cpr = lane / CPR;    // this lane's piece, and its row of each group of 32 / CPR
-  const uint8_t* kb = a.k + (int64_t)b * a.n_cap * row_bytes + g * D + cpc * 16;
-  const uint8_t* vb = a.v + (int64_t)b * a.n_cap * row_bytes + g * D + cpc * 16;
-  const float* sb = (lane < 16 ? a.ks : a.vs) + (int64_t)b * a.nblk * a.hkv + g;
-  const int32_t* ib = kl.idx + (int64_t)list * kl.idx_stride;
-  const int ni = (int)kl.ni, jump = (int)(kl.lo - kl.ni) - cnt;
-  auto position = [&](int s) -> int {              // of key slot lane % 16 of step s (a key behind the list: its last)
-    const int t = min(s * kQ8Keys + (lane & 15), n_keys - 1);
-    int p = t < ni ? t : (t < ni + cnt ? __ldg(ib + t - ni) : t + jump);
-    return min(max(p, 0), (int)a.n_cap - 1);
-  };
-  const uint32_t ring = smem_u32(q8sm) + warp * (kQ8Stages * q8_stage_bytes<D>());
-  auto issue = [&](int pos, uint32_t st) {
-#pragma unroll
-    for (int i = 0; i < kQ8Keys * CPR / 32; ++i) {
-      const int row = cpr + i * (32 / CPR);
-      const int64_t off = (int64_t)__shfl_sync(0xffffffffu, pos, row) * row_bytes;
-      cp_async16(st + q8_k_off<D>(row, cpc), kb + off, 16u);
-      cp_async16(st + kQ8Keys * D + q8_v_off<D>(row, cpc), vb + off, 16u);
-    }
-    cp_async4(st + 2 * kQ8Keys * D + lane * 4, sb + (int64_t)(pos >> a.bshift) * a.hkv);
-  };
-
-  float acc[2 * VW][NT][4];              // O^T tiles: dims (2 t, 2 t + 1) of the lane's D / 8, rows 2 tig, 2 tig + 1
-  float m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      m[nt][j] = -INFINITY;
-      l[nt][j] = 0.f;
-    }
-#pragma unroll
-  for (int t = 0; t < 2 * VW; ++t)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][nt][e] = 0.f;
-
-  int pos_n = 0, s_n = s_beg;            // the next step to issue, and its positions
-  uint32_t st_n = ring;                  // and the ring slot it goes to
-  const uint32_t ring_end = ring + kQ8Stages * q8_stage_bytes<D>();
-  auto advance = [&](uint32_t st) { return st + q8_stage_bytes<D>() == ring_end ? ring : st + q8_stage_bytes<D>(); };
-  auto issue_next = [&]() {
-    if (s_n < s_end) issue(pos_n, st_n);
-    cp_async_commit();                   // one group per step, empty past the end
-    s_n += kw;
-    st_n = advance(st_n);
-    if (s_n < s_end) pos_n = position(s_n);
-  };
-  if (s_n < s_end) pos_n = position(s_n);
-#pragma unroll
-  for (int i = 0; i < kQ8Stages - 1; ++i) issue_next();
   uint32_t st = ring;
   for (int s = s_beg; s < s_end; s += kw, st = advance(st)) {
     cp_async_wait<kQ8Stages - 2>();      // this lane's pieces of step s are here
@@ -346,42 +339,60 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         }
       }
 
-    // softmax: keys gid and gid + 8 (u), rows 2 tig and 2 tig + 1 (j)
-    const float lg = q8_log2(sc_cur);
+    // softmax: keys gid and gid + 8 (u), rows 2 tig and 2 tig + 1 (j). The weights come
+    // first, against m as it is; the row maxima (a reduction over 8 lanes) only when one of
+    // them says that m has to rise (at once on the first step: m is -inf).
     float ka[2], lv[2];
+    {
+      const float lg = __log2f(fmaxf(sc_cur, 0x1p-120f));      // within 2^-23 at powers of two; iv follows it
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      ka[u] = __shfl_sync(0xffffffffu, sc_cur, gid + 8 * u);
-      lv[u] = __shfl_sync(0xffffffffu, lg, 16 + gid + 8 * u);
+      for (int u = 0; u < 2; ++u) {
+        ka[u] = __shfl_sync(0xffffffffu, sc_cur, gid + 8 * u);
+        lv[u] = __shfl_sync(0xffffffffu, lg, 16 + gid + 8 * u) + kQ8Head;
+      }
     }
     const int t0 = s * kQ8Keys;
-    const bool cut = t0 + kQ8Keys > n_all;
-    float x[NT][2][2];
-    float top[NT][2];
-    bool raise = false;
+    const bool cut = t0 + kQ8Keys > n_all;                     // some row does not see some key
+    float wt[NT][2][2];
+    auto weights = [&]() -> float {
+      float top = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          x[nt][j][u] = (sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j]) * ka[u] * xs[nt][j];
-          if (cut && t0 + gid + 8 * u >= lim[nt][j]) x[nt][j][u] = -INFINITY;
-        }
-        float mx = fmaxf(x[nt][j][0] + lv[0], x[nt][j][1] + lv[1]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        top[nt][j] = mx;
-        raise |= mx > m[nt][j] + kQ8Lazy;
+          for (int u = 0; u < 2; ++u)
+            wt[nt][u][j] = fast_exp2(fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], lv[u] - m[nt][j]));
+      if (cut) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (t0 + gid + 8 * u >= lim[nt][j]) wt[nt][u][j] = 0.f;
       }
-    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        top = fmaxf(fmaxf(top, fmaxf(wt[nt][0][0], wt[nt][0][1])), fmaxf(wt[nt][1][0], wt[nt][1][1]));
+      return top;
+    };
+    if (__any_sync(0xffffffffu, weights() > kQ8Most)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float al[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float mn = fmaxf(m[nt][j], top[nt][j]);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float x = fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], lv[u] - kQ8Head);
+            if (t0 + gid + 8 * u < lim[nt][j]) mx = fmaxf(mx, x);
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[nt][j], mx);
           al[j] = mn == -INFINITY ? 1.f : fast_exp2(m[nt][j] - mn);
           m[nt][j] = mn;
           l[nt][j] *= al[j];
@@ -394,30 +405,23 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
           acc[t][nt][3] *= al[1];
         }
       }
+      weights();
     }
     uint32_t wf[NT][2], wl[F32 ? NT : 1][2];
+    const float iv[2] = {fast_exp2(-lv[0]), fast_exp2(-lv[1])};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float wt[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float mr = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          l[nt][j] += fast_exp2(x[nt][j][u] - mr);
-          wt[u][j] = fast_exp2(x[nt][j][u] + lv[u] - mr + kQ8Head);
-        }
-      }
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t h = f16x2_rn(wt[u][0], wt[u][1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) l[nt][j] = fmaf(wt[nt][u][j], iv[u], l[nt][j]);
+        const uint32_t h = f16x2_rn(wt[nt][u][0], wt[nt][u][1]);
         wf[nt][u] = movmatrix_t(h);
         if constexpr (F32) {
           const float2 hf = f16x2_to_float2(h);
-          wl[nt][u] = movmatrix_t(f16x2_rn(wt[u][0] - hf.x, wt[u][1] - hf.y));
+          wl[nt][u] = movmatrix_t(f16x2_rn(wt[nt][u][0] - hf.x, wt[nt][u][1] - hf.y));
         }
       }
-    }
 
     // O^T += Vc^T W^T
     uint32_t vr[4][VW];
