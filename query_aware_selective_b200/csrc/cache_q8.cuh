@@ -44,26 +44,30 @@ __device__ __forceinline__ void q8_widen4(uint32_t w, float* f) {
     const float2 b = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(w >> 16)));
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(w >> (8 * e));
+    // 0x4b000000 | (c + 128) is the float 2^23 + 128 + c
+    w ^= 0x80808080u;
+    f[0] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)) - 8388736.f;
+    f[1] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)) - 8388736.f;
+    f[2] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)) - 8388736.f;
+    f[3] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)) - 8388736.f;
   }
 }
-// four values as codes: nearest, ties to even, clamped to +-qmax
+// Four values times inv (a power of two) as codes: nearest, ties to even. The products fit
+// the format (|f inv| <= qmax); e4m3 saturates besides.
 template <int FMT>
-__device__ __forceinline__ uint32_t q8_narrow4(const float* f) {
+__device__ __forceinline__ uint32_t q8_narrow4(const float* f, float inv) {
   if constexpr (FMT == kQ8E4M3) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1] * inv), "f"(f[0] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3] * inv), "f"(f[2] * inv));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   } else {
-    uint32_t w = 0;
+    // 1.5 * 2^23 + c holds c's two's complement in its low bits; the product is exact, so
+    // the sum's rounding is the one to the nearest integer
+    uint32_t g[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = __float2int_rn(fminf(fmaxf(f[e], -127.f), 127.f));
-      w |= ((uint32_t)c & 0xffu) << (8 * e);
-    }
-    return w;
+    for (int e = 0; e < 4; ++e) g[e] = __float_as_uint(fmaf(f[e], inv, 12582912.f));
+    return __byte_perm(__byte_perm(g[0], g[1], 0x0040), __byte_perm(g[2], g[3], 0x0040), 0x5410);
   }
 }
 
@@ -91,6 +95,7 @@ struct CacheWriteArgs {
   const int64_t* seq_len;  // null, or [B]: rows end at seq_len[b]
   const int64_t* new_len;  // null, or [B]: new rows of sequence b
   int hkv, bshift;
+  bool wide;               // rows of x are 32-byte aligned
 };
 
 // Positions [start, end) that sequence b writes. False: nothing (an empty write, or
@@ -112,16 +117,31 @@ __device__ __forceinline__ bool q8_write_range(const CacheWriteArgs& a, int b, i
   return true;
 }
 
+// 32 bytes of global memory in one load (they are 32-byte aligned), or in two
+__device__ __forceinline__ void ld_global_32(const void* p, bool wide, uint32_t* w) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = ld_stream16(p), b = ld_stream16(static_cast<const uint8_t*>(p) + 16);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+
 // One CTA per (block of tokens, head, operand) of a sequence: block * D / 64 threads, so
-// that a thread holds 8 elements of each of 8 rows in registers and the block is read
+// that a thread holds 16 elements of each of 4 rows in registers and the block is read
 // once: load everything, take the maximum, scale, round, store. Bound by HBM (and by
 // launch and one memory latency for a single token). grid (blocks * 2 Hkv, B), heads
 // fastest: the CTAs that share rows run together, so DRAM pages are read whole.
+// 32768 tokens of 8 heads of 128 (201 MB): 33.7 us, 5.98 TB/s, with 32-byte loads; 39.1 us
+// with 16-byte loads of 8 elements a row and thread.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArgs a) {
-  constexpr int TPR = D / 8;                       // threads of a row
-  constexpr int W = 8 * sizeof(T) / 4;             // 32-bit words of 8 elements: 4 or 8
-  constexpr int NP = 8;                            // rows of a thread
+  constexpr int TPR = D / 16;                      // threads of a row
+  constexpr int W = 16 * sizeof(T) / 4;            // 32-bit words of 16 elements: 8 or 16
+  constexpr int NP = 4;                            // rows of a thread
   const uint32_t width = 2u * a.hkv, yb = blockIdx.x / width, col = blockIdx.x - yb * width;
   const int op = col >= (uint32_t)a.hkv, h = col - (op ? a.hkv : 0), b = blockIdx.y;
   int64_t start, end;
@@ -131,7 +151,7 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
   if (base >= end) return;
   const int block = 1 << a.bshift;
   const int row0 = threadIdx.x / TPR, piece = threadIdx.x % TPR, rpp = blockDim.x / TPR;
-  const T* src = static_cast<const T*>(op ? a.x[1] : a.x[0]) + (int64_t)b * a.bs[op] + (int64_t)h * D + piece * 8;
+  const T* src = static_cast<const T*>(op ? a.x[1] : a.x[0]) + (int64_t)b * a.bs[op] + (int64_t)h * D + piece * 16;
   const int64_t rs = a.rs[op];
   float* sc = a.scale[op] + ((int64_t)b * a.nblk + blk) * a.hkv + h;
   uint8_t* codes = a.codes[op] + ((int64_t)b * a.n_cap * a.hkv + h) * D;     // + position * Hkv * D
@@ -145,9 +165,10 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
     const int64_t pos = base + r;
     mine[p] = r < block && pos >= start && pos < end;
 #pragma unroll
-    for (int q = 0; q < W / 4; ++q) {
-      const uint4 v = mine[p] ? ld_stream16(src + (pos - start) * rs + q * 4) : make_uint4(0u, 0u, 0u, 0u);
-      x[p][4 * q] = v.x; x[p][4 * q + 1] = v.y; x[p][4 * q + 2] = v.z; x[p][4 * q + 3] = v.w;
+    for (int w = 0; w < W; ++w) x[p][w] = 0u;
+    if (mine[p]) {
+#pragma unroll
+      for (int q = 0; q < W / 8; ++q) ld_global_32(src + (pos - start) * rs + q * 8, a.wide, x[p] + q * 8);
     }
   }
   float old = start > base ? *sc : 0.f;            // rows before the write hold their values under it
@@ -176,41 +197,50 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
     }
   if constexpr (sizeof(T) == 2) mx = max(mx & 0xffff0000u, mx << 16);
   mx = block_max(mx);
-  if (mx >= 0x7f800000u) {
-    // not finite: NaN becomes 0, an infinity the largest code of a block scaled by its
-    // finite values; recorded for the host
-    if (threadIdx.x == 0) record_status(7u, 705);
-    uint32_t fin = 0;
+  const bool finite = mx < 0x7f800000u;
+  // applies fn to the bits of every element and puts them back
+  auto each = [&](auto fn) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int e = 0; e < (sizeof(T) == 2 ? 2 : 1); ++e) {
-          const uint32_t v = sizeof(T) == 4 ? x[p][w] : (e ? x[p][w] & 0xffff0000u : x[p][w] << 16);
-          const uint32_t m = v & 0x7fffffffu;
-          if (m > 0x7f800000u) x[p][w] &= sizeof(T) == 4 ? 0u : (e ? 0x0000ffffu : 0xffff0000u);
-          else if (m < 0x7f800000u) fin = max(fin, m);
-        }
+      for (int w = 0; w < W; ++w) {
+        if constexpr (sizeof(T) == 4) x[p][w] = fn(x[p][w]);
+        else x[p][w] = (fn(x[p][w] & 0xffff0000u) & 0xffff0000u) | (fn(x[p][w] << 16) >> 16);
+      }
+  };
+  if (!finite) {
+    // NaN becomes 0, an infinity the largest code of a block scaled by its finite values;
+    // recorded for the host
+    if (threadIdx.x == 0) record_status(7u, 705);
+    uint32_t fin = 0;
+    each([&](uint32_t v) {
+      const uint32_t m = v & 0x7fffffffu;
+      if (m < 0x7f800000u) fin = max(fin, m);
+      return m > 0x7f800000u ? 0u : v;
+    });
     mx = block_max(fin);
   }
   const float s = fmaxf(q8_scale_of<FMT>(mx), old);
   const float inv = 1.f / s;                       // exact: powers of two
+  if (!finite) {
+    const uint32_t top = __float_as_uint((FMT == kQ8E4M3 ? 448.f : 127.f) * s);
+    each([&](uint32_t v) { return (v & 0x7fffffffu) == 0x7f800000u ? (v & 0x80000000u) | top : v; });
+  }
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     if (!mine[p]) continue;
-    float f[8];
+    uint32_t c[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(T) == 2)
-        f[e] = __uint_as_float((e & 1) ? x[p][e / 2] & 0xffff0000u : x[p][e / 2] << 16) * inv;
-      else
-        f[e] = __uint_as_float(x[p][e]) * inv;
+    for (int q = 0; q < 4; ++q) {
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) f[e] = __uint_as_float(x[p][4 * q + e]);
+        else f[e] = __uint_as_float((e & 1) ? x[p][2 * q + e / 2] & 0xffff0000u : x[p][2 * q + e / 2] << 16);
+      }
+      c[q] = q8_narrow4<FMT>(f, inv);
     }
-    uint2 w;
-    w.x = q8_narrow4<FMT>(f);
-    w.y = q8_narrow4<FMT>(f + 4);
-    *reinterpret_cast<uint2*>(codes + (base + row0 + p * rpp) * cs + piece * 8) = w;
+    *reinterpret_cast<uint4*>(codes + (base + row0 + p * rpp) * cs + piece * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
   if (start > base && s > old) {
     // the block's scale grew: the rows already there move to it
@@ -224,9 +254,7 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
       for (int q = 0; q < 4; ++q) {
         float f[4];
         q8_widen4<FMT>(w[q], f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] *= ratio;
-        w[q] = q8_narrow4<FMT>(f);
+        w[q] = q8_narrow4<FMT>(f, ratio);
       }
       *p = v;
     }
@@ -280,44 +308,85 @@ struct CacheReadArgs {
 
 constexpr int kReadThreads = 256, kReadPer = 4;
 
+// How threads lie over result rows of `pieces` 32-byte pieces: a CTA takes up to 256
+// columns (more: several CTAs side by side) and as many rows a pass as fit, kReadPer
+// passes. A thread keeps its column, so only rows change from piece to piece.
+struct ReadTile {
+  int cols, col_ctas, rows;   // columns and column CTAs, rows of a pass
+  __host__ __device__ explicit ReadTile(int pieces) {
+    cols = pieces < kReadThreads ? pieces : kReadThreads;
+    col_ctas = (pieces + kReadThreads - 1) / kReadThreads;
+    rows = kReadThreads / cols;
+  }
+};
+
+// Codes at pos[u] (negative: zeros) of a thread's column, times their scales, to rows
+// row0 + u * rows of the result.
+template <typename T, int FMT>
+__device__ __forceinline__ void q8_move(const uint8_t* codes, const float* scale, uint32_t row_bytes, int hkv,
+                                        int bshift, const int (&pos)[kReadPer], T* out, int64_t row0, int rows,
+                                        int64_t n) {
+  constexpr int N = 32 / sizeof(T);
+  uint32_t c[kReadPer][N / 4];
+  float s[kReadPer];
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    // (a row that is not wanted loads row 0: a branch here would put each conversion
+    // behind its own load)
+    const uint32_t at = max(pos[u], 0);
+    q8_load_codes<N>(codes + (uint64_t)at * row_bytes, c[u]);
+    s[u] = __ldg(scale + (uint64_t)(at >> bshift) * (uint32_t)hkv);
+  }
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    if (pos[u] < 0) {
+      s[u] = 0.f;
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) c[u][q] = 0u;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kReadPer; ++u) {
+    const int64_t r = row0 + u * rows;
+    if (r < n) q8_widen_store<T, FMT>(c[u], s[u], out + r * row_bytes);      // row_bytes elements a row
+  }
+}
+
 // Row (b, r) of the result is cache row start + r, or idx[b, r] (zeros where that is not a
-// row of the cache). A thread makes 32 bytes of the result from 16 (8) codes, kReadPer of
-// them with their loads in flight together. Bound by HBM. grid (pieces, B, operands).
+// row of the cache). A thread makes 32 bytes of the result from 16 (8) codes, kReadPer
+// rows with their loads in flight together (2, 4, 8 rows: 48, 37.6, 41.7 us for 32000 rows
+// of 8 heads of 128). Bound by HBM, two thirds of it writes: 197 MB in 37.6 us, 5.23 TB/s;
+// a device copy of 262 MB takes 45.5 us (5.76 TB/s) and a fill of 131 MB 24.9 us (5.26).
+// grid (row tiles * column CTAs, B, operands).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const CacheReadArgs a) {
   constexpr int N = 32 / sizeof(T);
   const int op = blockIdx.z, b = blockIdx.y;
   T* out = static_cast<T*>(a.out[op]);
   if (!out) return;
-  const int per_row = a.hkv * a.d / N;
-  const int64_t total = a.n * per_row;
-  const int64_t i0 = (int64_t)blockIdx.x * (kReadThreads * kReadPer) + threadIdx.x;
-  uint32_t c[kReadPer][N / 4];
-  float s[kReadPer];
+  const uint32_t row_bytes = (uint32_t)(a.hkv * a.d);
+  const ReadTile tile(row_bytes / N);
+  const int rt = blockIdx.x / tile.col_ctas, cc = blockIdx.x - rt * tile.col_ctas;
+  const int tr = threadIdx.x / tile.cols, col = cc * kReadThreads + threadIdx.x - tr * tile.cols;
+  if (tr >= tile.rows || col * N >= row_bytes) return;
+  const int64_t row0 = (int64_t)rt * (tile.rows * kReadPer) + tr;
+  int pos[kReadPer];
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
-    const int64_t i = i0 + u * kReadThreads;
-    s[u] = 0.f;
-#pragma unroll
-    for (int q = 0; q < N / 4; ++q) c[u][q] = 0u;
-    if (i >= total) continue;
-    const int64_t r = total < ((int64_t)1 << 31) ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
-    const int w = (int)(i - r * per_row);
-    const int64_t pos = a.idx ? (int64_t)a.idx[(int64_t)b * a.n + r] : a.start + r;
-    if (pos < 0 || pos >= a.n_cap) continue;
-    q8_load_codes<N>(a.codes[op] + ((int64_t)b * a.n_cap + pos) * a.hkv * a.d + w * N, c[u]);
-    s[u] = __ldg(a.scale[op] + ((int64_t)b * a.nblk + (pos >> a.bshift)) * a.hkv + w * N / a.d);
+    const int64_t r = row0 + u * tile.rows;
+    pos[u] = r < a.n ? (a.idx ? __ldg(a.idx + (int64_t)b * a.n + r) : (int)(a.start + r)) : -1;
   }
 #pragma unroll
-  for (int u = 0; u < kReadPer; ++u) {
-    const int64_t i = i0 + u * kReadThreads;
-    if (i < total) q8_widen_store<T, FMT>(c[u], s[u], out + ((int64_t)b * total + i) * N);
-  }
+  for (int u = 0; u < kReadPer; ++u) pos[u] = pos[u] < a.n_cap ? pos[u] : -1;
+  q8_move<T, FMT>(a.codes[op] + (int64_t)b * a.n_cap * row_bytes + col * N,
+                  a.scale[op] + (int64_t)b * a.nblk * a.hkv + col * N / a.d, row_bytes, a.hkv, a.bshift, pos,
+                  out + (int64_t)b * a.n * row_bytes + col * N, row0, tile.rows, a.n);
 }
 
 // The whole key list of a chunk (initial, selected, local and the chunk itself; one list
 // per sequence, or one per KV head) as bf16 rows [B, t_pad, Hkv, 128] for the tensor-core
 // attention; rows behind the list are zeros, up to t_pad (a multiple of the key tile).
+// grid as above.
 struct CacheStageArgs {
   const uint8_t* codes[2];
   const float* scale[2];
@@ -330,32 +399,24 @@ struct CacheStageArgs {
 template <int FMT>
 __global__ void __launch_bounds__(kReadThreads) cache_stage_q8_kernel(const CacheStageArgs a) {
   const int op = blockIdx.z, b = blockIdx.y;
-  const int per_row = a.hkv * 8;                        // 16-code pieces of a token
-  const int64_t total = a.t_pad * per_row;
-  const int64_t i0 = (int64_t)blockIdx.x * (kReadThreads * kReadPer) + threadIdx.x;
-  uint32_t c[kReadPer][4];
-  float s[kReadPer];
+  const uint32_t row_bytes = (uint32_t)(a.hkv * 128);
+  const ReadTile tile(row_bytes / 16);
+  const int rt = blockIdx.x / tile.col_ctas, cc = blockIdx.x - rt * tile.col_ctas;
+  const int tr = threadIdx.x / tile.cols, col = cc * kReadThreads + threadIdx.x - tr * tile.cols;
+  if (tr >= tile.rows || col * 16 >= row_bytes) return;
+  const int64_t row0 = (int64_t)rt * (tile.rows * kReadPer) + tr;
+  const int g = col >> 3, list = a.lists > 1 ? b * a.lists + g : b;
+  const int cnt = min(max(a.keys.count[list], 0), (int)a.keys.idx_stride);
+  const int64_t n_keys = a.keys.ni + cnt + (a.c0 - a.keys.lo) + a.lq;
+  int pos[kReadPer];
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
-    const int64_t i = i0 + u * kReadThreads;
-    s[u] = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) c[u][q] = 0u;
-    if (i >= total) continue;
-    const int64_t t = total < ((int64_t)1 << 31) ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
-    const int w = (int)(i - t * per_row), g = w >> 3;
-    const int list = a.lists > 1 ? b * a.lists + g : b;
-    const int cnt = min(max(a.keys.count[list], 0), (int)a.keys.idx_stride);
-    if (t >= a.keys.ni + cnt + (a.c0 - a.keys.lo) + a.lq) continue;
-    const int64_t pos = a.keys.pos(list, cnt, t);
-    q8_load_codes<16>(a.codes[op] + ((int64_t)b * a.n_cap + pos) * a.hkv * 128 + w * 16, c[u]);
-    s[u] = __ldg(a.scale[op] + ((int64_t)b * a.nblk + (pos >> a.bshift)) * a.hkv + g);
+    const int64_t t = row0 + u * tile.rows;
+    pos[u] = t < n_keys ? (int)a.keys.pos(list, cnt, t) : -1;
   }
-#pragma unroll
-  for (int u = 0; u < kReadPer; ++u) {
-    const int64_t i = i0 + u * kReadThreads;
-    if (i < total) q8_widen_store<__nv_bfloat16, FMT>(c[u], s[u], a.out[op] + ((int64_t)b * total + i) * 16);
-  }
+  q8_move<__nv_bfloat16, FMT>(a.codes[op] + (int64_t)b * a.n_cap * row_bytes + col * 16,
+                              a.scale[op] + (int64_t)b * a.nblk * a.hkv + g, row_bytes, a.hkv, a.bshift, pos,
+                              a.out[op] + (int64_t)b * a.t_pad * row_bytes + col * 16, row0, tile.rows, a.t_pad);
 }
 
 }  // namespace esa

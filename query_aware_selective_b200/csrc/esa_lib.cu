@@ -1228,6 +1228,8 @@ esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int6
   a.new_len = new_len;
   a.hkv = c.hkv;
   a.bshift = log2_of(c.block);
+  const int64_t wide = 2 * vec;
+  a.wide = aligned(k, 32) && aligned(v, 32) && !(krs % wide || vrs % wide || kbs % wide || vbs % wide);
   // blocks that rows consecutive tokens can touch (with device lengths: from any offset)
   const int64_t blocks = seq_len ? (rows + c.block - 2) / c.block + 1
                                  : (start + rows - 1) / c.block - start / c.block + 1;
@@ -1345,7 +1347,8 @@ esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, i
   a.hkv = c.hkv;
   a.lists = lists;
   a.bshift = log2_of(c.block);
-  const dim3 sgrid((unsigned)cdiv(t_pad * c.hkv * 8, esa::kReadThreads * esa::kReadPer), c.batch, 2);
+  const esa::ReadTile tile(c.hkv * 8);
+  const dim3 sgrid((unsigned)(cdiv(t_pad, tile.rows * esa::kReadPer) * tile.col_ctas), c.batch, 2);
   if (c.format == ESA_Q8_E4M3) esa::cache_stage_q8_kernel<esa::kQ8E4M3><<<sgrid, esa::kReadThreads, 0, s>>>(a);
   else esa::cache_stage_q8_kernel<esa::kQ8Int8><<<sgrid, esa::kReadThreads, 0, s>>>(a);
   ESA_LAUNCH_CHECK("cache_stage_q8_kernel");
@@ -1479,8 +1482,8 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
   a.hkv = cache.hkv;
   a.d = cache.head_dim;
   a.bshift = log2_of(cache.block);
-  const int64_t codes = dt == ESA_BF16 ? 16 : 8;            // of a thread's 32-byte store
-  const int64_t ctas = cdiv(rows * (cache.hkv * cache.head_dim / codes), esa::kReadThreads * esa::kReadPer);
+  const esa::ReadTile tile(cache.hkv * cache.head_dim / (dt == ESA_BF16 ? 16 : 8));
+  const int64_t ctas = cdiv(rows, tile.rows * esa::kReadPer) * tile.col_ctas;
   if (ctas >= ((int64_t)1 << 31)) return fail(ESA_ERR_UNSUPPORTED, "too many rows in one read");
   const dim3 grid((unsigned)ctas, cache.batch, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
