@@ -19,6 +19,7 @@
 #include "attn_decode.cuh"
 #include "attn_pp.cuh"
 #include "attn_q8.cuh"
+#include "attn_q8_tc.cuh"
 #include "attn_simt.cuh"
 #include "attn_tc.cuh"
 #include "cache_q8.cuh"
@@ -1313,6 +1314,43 @@ esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int nt, dim3
                  : launch_attn_q8<T, D, esa::kQ8Int8, 2>(a, grid, csize, s);
 }
 
+template <int FMT, int RT>
+esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cudaStream_t s) {
+  using Sh = esa::QtShape<FMT, RT>;
+  static const char what = 0;
+  const esa_status_t st =
+      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_tc_kernel<FMT, RT>, Sh::kSmem); });
+  if (st != ESA_OK) return st;
+  a.hc = 1;
+  a.tiles = (int)cdiv((int64_t)a.lq * a.G, RT);
+  const int64_t units = (int64_t)batch * a.hkv * a.tiles, slots = 148 * Sh::kCtas;
+  if ((int64_t)a.hkv * a.tiles > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
+  const int csize =
+      (int)std::max<int64_t>(1, std::min<int64_t>({8, slots / units, cdiv(n_keys, esa::kQtKeys)}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(csize, a.hkv * a.tiles, batch);
+  cfg.blockDim = dim3(esa::kQtThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = csize;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  ESA_CUDA(cudaLaunchKernelEx(&cfg, esa::attn_q8_tc_kernel<FMT, RT>, a));
+  ESA_LAUNCH_CHECK("attn_q8_tc_kernel");
+  return ok();
+}
+template <int FMT>
+esa_status_t dispatch_attn_q8_tc(const esa::AttnQ8Args& a, int32_t batch, int64_t n_keys, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.lq * a.G;
+  if (rows <= 4) return launch_attn_q8_tc<FMT, 4>(a, batch, n_keys, s);
+  if (rows <= 8) return launch_attn_q8_tc<FMT, 8>(a, batch, n_keys, s);
+  return launch_attn_q8_tc<FMT, 16>(a, batch, n_keys, s);
+}
+
 // The chunk form: the key list dequantised into the workspace, then attn_tc_kernel.
 esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, int64_t c0, int32_t hq,
                            const esa::KeyList& keys, int lists, const esa_params_t& p, float sl2, void* o, float* lse,
@@ -1431,6 +1469,11 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
   a.hc = pl.hc;
   a.tiles = (int)tiles;
   a.scale_log2 = sl2;
+  if (dt == ESA_BF16 && c.head_dim == 128) {
+    const int64_t n_keys = r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq;
+    return c.format == ESA_Q8_E4M3 ? dispatch_attn_q8_tc<esa::kQ8E4M3>(a, c.batch, n_keys, s)
+                                   : dispatch_attn_q8_tc<esa::kQ8Int8>(a, c.batch, n_keys, s);
+  }
   const dim3 grid((unsigned)pl.csize, (unsigned)(tiles * (c.hkv / pl.hc)), c.batch);
   if (dt == ESA_BF16)
     return c.head_dim == 128 ? dispatch_attn_q8<__nv_bfloat16, 128>(a, c.format, nt, grid, pl.csize, s)
