@@ -465,7 +465,7 @@ class CacheQ8:
     block of tokens and head; a value is code * scale. The tensors are the caller's (see
     cache_q8 for new ones), are checked once, here, and stay the ones of this cache."""
 
-    __slots__ = ("_k", "_k_scale", "_v", "_v_scale", "_c")
+    __slots__ = ("_k", "_k_scale", "_v", "_v_scale", "_c", "_dev", "_shape")
 
     def __init__(self, k: torch.Tensor, k_scale: torch.Tensor, v: torch.Tensor, v_scale: torch.Tensor, block: int):
         _dev(k, k_scale, v, v_scale)
@@ -483,6 +483,7 @@ class CacheQ8:
         self._k, self._k_scale, self._v, self._v_scale = k, k_scale, v, v_scale
         self._c = EsaCacheQ8(_ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), n_cap, b, hkv, d, block,
                              Q8_FORMATS[k.dtype])
+        self._dev, self._shape = k.get_device(), (b, hkv, d)
 
     k = property(lambda self: self._k)
     k_scale = property(lambda self: self._k_scale)
@@ -503,54 +504,67 @@ def cache_q8(batch: int, n_cap: int, hkv: int, head_dim: int, dtype: torch.dtype
     return CacheQ8(codes(), scales(), codes(), scales(), block)
 
 
+# (The helpers below are written for few interpreter steps: a call on a small batch takes
+# longer here than on the GPU.)
+_DTYPE_CODES = {torch.float32: ESA_F32, torch.bfloat16: ESA_BF16}
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
 def _q8_call(cache: CacheQ8, where: str, *args):
     """Call `where` with args and the current stream of the cache's device, under that
-    device."""
-    dev = cache._k.device.index
-    fn = getattr(load(), where)
-    if torch.cuda.current_device() == dev:
-        # the handle alone: torch.cuda.current_stream() builds a Stream object (3 us)
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    device. (The raw stream handle: torch.cuda.current_stream() builds a Stream, 3 us.)"""
+    dev = cache._dev
+    fn = getattr(_lib or load(), where)
+    if _current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if st != ESA_OK:
+            st = fn(*args, _raw_stream(dev))
+    if st:
         _check(st, where)
 
 
-def _q8_empty(shape, dtype, device) -> torch.Tensor:
+def _q8_dtype(t: torch.Tensor) -> int:
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _q8_empty(shape, dtype, cache: CacheQ8) -> torch.Tensor:
     """torch.empty of a shape of 3 or 4 (empty_strided takes half its host time)."""
-    strides = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else \
-        (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    n = shape[-1]
+    strides = (shape[1] * n, n, 1) if len(shape) == 3 else (shape[1] * shape[2] * n, shape[2] * n, n, 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=cache._k.device)
 
 
-def _q8_tensor(t: torch.Tensor, name: str, cache: CacheQ8, dtype, shape):
-    """t as an argument of a call on the cache: its device, dtype, shape, contiguous."""
-    if t.device != cache._k.device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+def _q8_tensor(t: torch.Tensor, name: str, cache: CacheQ8, dtype, shape) -> int:
+    """t as an argument of a call on the cache: its device, dtype, shape, contiguous. Returns
+    its address."""
+    if t.get_device() != cache._dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the cache's device")
-
-
-def _q8_rows(x: torch.Tensor, name: str, cache: CacheQ8):
-    """New rows [B, T, Hkv, D]: batch and row strides free, each row contiguous."""
-    c = cache._c
-    if x.device != cache._k.device:
-        raise ValueError(f"{name} must be on the cache's device (no CPU path)")
-    if x.dim() != 4 or x.shape[0] != c.batch or x.shape[2] != c.hkv or x.shape[3] != c.head_dim:
-        raise ValueError(f"{name} must be [B, T, Hkv, D] = [{c.batch}, T, {c.hkv}, {c.head_dim}]")
-    if x.stride(3) != 1 or (c.hkv > 1 and x.stride(2) != c.head_dim):
-        raise ValueError(f"each row of {name} must be contiguous [Hkv, D]")
+    return t.data_ptr()
 
 
 def _q8_write(where: str, cache: CacheQ8, k: torch.Tensor, v: torch.Tensor, *tail):
-    _q8_rows(k, "k", cache)
-    _q8_rows(v, "v", cache)
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("k and v must have the same shape and dtype")
+    """k, v: new rows [B, T, Hkv, D]: batch and row strides free, each row contiguous."""
+    b, h, d = cache._shape
+    shape = k.shape
+    if len(shape) != 4 or shape[0] != b or shape[2] != h or shape[3] != d or v.shape != shape or v.dtype is not k.dtype:
+        raise ValueError(f"k and v must be [B, T, Hkv, D] = [{b}, T, {h}, {d}] of one dtype")
+    if k.get_device() != cache._dev or v.get_device() != cache._dev:
+        raise ValueError("k and v must be on the cache's device (no CPU path)")
+    kb, kr, kh, ke = k.stride()
+    vb, vr, vh, ve = v.stride()
+    if ke != 1 or ve != 1 or (h > 1 and (kh != d or vh != d)):
+        raise ValueError("each row of k and v must be contiguous [Hkv, D]")
+    t = shape[1]
     # a stride that no second row or sequence uses may be anything: pass one that is aligned
-    kb, kr, vb, vr = (x.stride(i) if x.shape[i] > 1 else c for x in (k, v)
-                      for i, c in ((0, 0), (1, cache._c.hkv * cache._c.head_dim)))
-    _q8_call(cache, where, _ptr(k), _ptr(v), _dtype_code(k), k.shape[1], kb, kr, vb, vr, cache._c, *tail)
+    if t <= 1:
+        kr = vr = h * d
+    if b <= 1:
+        kb = vb = 0
+    _q8_call(cache, where, k.data_ptr(), v.data_ptr(), _q8_dtype(k), t, kb, kr, vb, vr, cache._c, *tail)
 
 
 def cache_write_q8(cache: CacheQ8, k: torch.Tensor, v: torch.Tensor, start: int) -> None:
@@ -563,11 +577,9 @@ def cache_write_q8_varlen(cache: CacheQ8, k: torch.Tensor, v: torch.Tensor, seq_
                           new_len: Optional[torch.Tensor] = None) -> None:
     """esa_cache_write_q8_varlen: sequence b's rows (the first new_len[b] of its T, or all)
     into positions [seq_len[b] - new_len[b], seq_len[b]). Lengths: int64 [B] on the device."""
-    b = cache._c.batch
-    _q8_tensor(seq_len, "seq_len", cache, torch.int64, (b,))
-    if new_len is not None:
-        _q8_tensor(new_len, "new_len", cache, torch.int64, (b,))
-    _q8_write("esa_cache_write_q8_varlen", cache, k, v, _ptr(seq_len), _ptr(new_len))
+    shape = (cache._shape[0],)
+    _q8_write("esa_cache_write_q8_varlen", cache, k, v, _q8_tensor(seq_len, "seq_len", cache, torch.int64, shape),
+              None if new_len is None else _q8_tensor(new_len, "new_len", cache, torch.int64, shape))
 
 
 def cache_read_q8(cache: CacheQ8, start: int = 0, rows: Optional[int] = None, idx: Optional[torch.Tensor] = None,
@@ -576,58 +588,71 @@ def cache_read_q8(cache: CacheQ8, start: int = 0, rows: Optional[int] = None, id
     """esa_cache_read_q8: the values of positions [start, start + rows) (to the end of the
     cache without rows), or of idx [B, n] int32 (outside the cache: zeros).
     Returns (k [B, n, Hkv, D] or None, v or None) of dtype f32 or bf16."""
-    c = cache._c
-    if dtype not in (torch.float32, torch.bfloat16):
+    b, h, d = cache._shape
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
+    where = None
     if idx is not None:
         if start != 0 or rows is not None:
             raise ValueError("idx excludes start and rows")
-        n = idx.shape[-1]
-        _q8_tensor(idx, "idx", cache, torch.int32, (c.batch, n))
+        n = idx.shape[-1] if idx.dim() else 0
+        where = _q8_tensor(idx, "idx", cache, torch.int32, (b, n))
     else:
-        n = c.n_cap - start if rows is None else rows
-        if start < 0 or n < 0 or start + n > c.n_cap:
+        n = cache._c.n_cap - start if rows is None else rows
+        if start < 0 or n < 0 or start + n > cache._c.n_cap:
             raise ValueError("need 0 <= start and start + rows <= n_cap")
-    shape = (c.batch, n, c.hkv, c.head_dim)
-    got = []
-    for out, want, name in ((k_out, want_k, "k_out"), (v_out, want_v, "v_out")):
-        if not want:
-            out = None
-        elif out is None:
-            out = _q8_empty(shape, dtype, cache._k.device)
-        else:
-            _q8_tensor(out, name, cache, dtype, shape)
-        got.append(out)
-    _q8_call(cache, "esa_cache_read_q8", c, start, n, _ptr(idx), _ptr(got[0]), _ptr(got[1]),
-             ESA_BF16 if dtype == torch.bfloat16 else ESA_F32)
-    return got[0], got[1]
-
-
-def _q8_attn_args(q, cache: CacheQ8, idx, count, p: EsaParams, want_lse, out, lse):
-    """Checks and outputs shared by the attention calls; returns (lists, out, lse)."""
-    c = cache._c
-    if q.dim() != 4 or q.shape[0] != c.batch or q.shape[3] != c.head_dim:
-        raise ValueError(f"q must be [B, Lq, Hq, D] = [{c.batch}, Lq, Hq, {c.head_dim}]")
-    if q.device != cache._k.device or not q.is_contiguous():
-        raise ValueError("q must be contiguous and on the cache's device (no CPU path)")
-    lists = count.shape[1] if count.dim() == 2 else 1
-    if count.dim() == 2:
-        _q8_tensor(count, "count", cache, torch.int32, (c.batch, lists))
-        _q8_tensor(idx, "idx", cache, torch.int32, (c.batch, lists, p.topk))
+    shape = (b, n, h, d)
+    kp = vp = None
+    if not want_k:
+        k_out = None
+    elif k_out is None:
+        k_out = _q8_empty(shape, dtype, cache)
+        kp = k_out.data_ptr()
     else:
-        _q8_tensor(count, "count", cache, torch.int32, (c.batch,))
-        _q8_tensor(idx, "idx", cache, torch.int32, (c.batch, p.topk))
+        kp = _q8_tensor(k_out, "k_out", cache, dtype, shape)
+    if not want_v:
+        v_out = None
+    elif v_out is None:
+        v_out = _q8_empty(shape, dtype, cache)
+        vp = v_out.data_ptr()
+    else:
+        vp = _q8_tensor(v_out, "v_out", cache, dtype, shape)
+    _q8_call(cache, "esa_cache_read_q8", cache._c, start, n, where, kp, vp, code)
+    return k_out, v_out
+
+
+def _q8_attn(q, cache: CacheQ8, idx, count, p: EsaParams, want_lse, out, lse):
+    """Checks and outputs shared by the attention calls. Returns out, lse and the addresses
+    of q, idx, count, out, lse, and the number of lists."""
+    b, _, d = cache._shape
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != b or shape[3] != d:
+        raise ValueError(f"q must be [B, Lq, Hq, D] = [{b}, Lq, Hq, {d}]")
+    if q.get_device() != cache._dev or not q.is_contiguous():
+        raise ValueError("q must be contiguous and on the cache's device (no CPU path)")
+    if count.dim() == 2:
+        lists = count.shape[1]
+        cp = _q8_tensor(count, "count", cache, torch.int32, (b, lists))
+        ip = _q8_tensor(idx, "idx", cache, torch.int32, (b, lists, p.topk))
+    else:
+        lists = 1
+        cp = _q8_tensor(count, "count", cache, torch.int32, (b,))
+        ip = _q8_tensor(idx, "idx", cache, torch.int32, (b, p.topk))
     if out is None:
         out = torch.empty_like(q)
+        op = out.data_ptr()
     else:
-        _q8_tensor(out, "out", cache, q.dtype, q.shape)
+        op = _q8_tensor(out, "out", cache, q.dtype, shape)
+    lp = None
     if not want_lse:
         lse = None
     elif lse is None:
-        lse = _q8_empty(q.shape[:3], torch.float32, q.device)
+        lse = _q8_empty(shape[:3], torch.float32, cache)
+        lp = lse.data_ptr()
     else:
-        _q8_tensor(lse, "lse", cache, torch.float32, q.shape[:3])
-    return lists, out, lse
+        lp = _q8_tensor(lse, "lse", cache, torch.float32, shape[:3])
+    return out, lse, q.data_ptr(), ip, cp, op, lp, lists
 
 
 def sparse_attn_q8_workspace_size(batch, lq, c0, hq, hkv, d, dtype_code, p: EsaParams) -> int:
@@ -640,16 +665,16 @@ def sparse_attn_q8(q: torch.Tensor, cache: CacheQ8, c0: int, idx: torch.Tensor, 
     """esa_sparse_attn_q8: q [B, Lq, Hq, D] at positions [c0, c0 + Lq) over the cache's
     initial + idx[:count] + local tokens; idx [B, topk], count [B] int32, or [B, L, topk] and
     [B, L] with L = 1 or Hkv (a list per KV head). Returns (o like q, lse [B, Lq, Hq] or None)."""
-    lists, out, lse = _q8_attn_args(q, cache, idx, count, p, want_lse, out, lse)
-    c, (b, lq, hq, d), dt = cache._c, q.shape, _dtype_code(q)
+    out, lse, qp, ip, cp, op, lp, lists = _q8_attn(q, cache, idx, count, p, want_lse, out, lse)
+    b, lq, hq, d = q.shape
+    dt = _q8_dtype(q)
     wp, wn = None, 0
     if lq > 1:                 # a single query needs no workspace
-        if workspace is not None and workspace.device != q.device:
+        if workspace is not None and workspace.get_device() != cache._dev:
             raise ValueError("the workspace must be on the cache's device")
-        ws = _workspace(sparse_attn_q8_workspace_size(b, lq, c0, hq, c.hkv, d, dt, p), q.device, workspace)
+        ws = _workspace(sparse_attn_q8_workspace_size(b, lq, c0, hq, cache._shape[1], d, dt, p), q.device, workspace)
         wp, wn = _ws_ptr(ws)
-    _q8_call(cache, "esa_sparse_attn_q8", _ptr(q), dt, c, lq, c0, hq, _ptr(idx), _ptr(count), lists, p, scale,
-             _ptr(out), _ptr(lse), wp, wn)
+    _q8_call(cache, "esa_sparse_attn_q8", qp, dt, cache._c, lq, c0, hq, ip, cp, lists, p, scale, op, lp, wp, wn)
     return out, lse
 
 
@@ -658,12 +683,12 @@ def sparse_attn_q8_varlen(q: torch.Tensor, cache: CacheQ8, seq_len: torch.Tensor
                           out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
     """esa_sparse_attn_q8_varlen: one query per sequence, q [B, 1, Hq, D], at position
     seq_len[b] - 1 (int64 [B] on the device). Lists and results as sparse_attn_q8."""
-    lists, out, lse = _q8_attn_args(q, cache, idx, count, p, want_lse, out, lse)
+    out, lse, qp, ip, cp, op, lp, lists = _q8_attn(q, cache, idx, count, p, want_lse, out, lse)
     if q.shape[1] != 1:
         raise ValueError("one query per sequence")
-    _q8_tensor(seq_len, "seq_len", cache, torch.int64, (cache._c.batch,))
-    _q8_call(cache, "esa_sparse_attn_q8_varlen", _ptr(q), _dtype_code(q), cache._c, _ptr(seq_len), q.shape[2],
-             _ptr(idx), _ptr(count), lists, p, scale, _ptr(out), _ptr(lse))
+    _q8_call(cache, "esa_sparse_attn_q8_varlen", qp, _q8_dtype(q), cache._c,
+             _q8_tensor(seq_len, "seq_len", cache, torch.int64, (cache._shape[0],)), q.shape[2], ip, cp, lists, p,
+             scale, op, lp)
     return out, lse
 
 

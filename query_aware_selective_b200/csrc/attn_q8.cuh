@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   const int n_keys = n_prior + (r0 + nrow - 1) / a.G + 1;      // that the tile's last row attends
   const int n_all = n_prior + i_first + 1;                     // that every row of the tile attends
   const int steps = (n_keys + kQ8Keys - 1) / kQ8Keys;
-  const int s_end = (int)((int64_t)steps * (rank + 1) / csize);
-  const int s_beg = (int)((int64_t)steps * rank / csize) + kp;
+  // the warps' shares of the steps interleave: each gets its part of the scattered keys
+  const int s_beg = rank * kw + kp, s_end = steps, s_inc = csize * kw;
 
   // ---- the stream: the warp's own ring of kQ8Stages steps in shared memory, filled by
   // 16-byte cp.async (8 or 4 lanes a row), positions looked up one step before that
@@ -213,11 +213,12 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   const float* sb = (lane < 16 ? a.ks : a.vs) + (int64_t)b * a.nblk * a.hkv + g;
   const int32_t* ib = kl.idx + (int64_t)list * kl.idx_stride;
   const int ni = (int)kl.ni, jump = (int)(kl.lo - kl.ni) - cnt;
-  auto position = [&](int s) -> int {              // of key slot lane % 16 of step s (a key behind the list: its last)
-    const int t = min(s * kQ8Keys + (lane & 15), n_keys - 1);
-    int p = t < ni ? t : (t < ni + cnt ? __ldg(ib + t - ni) : t + jump);
-    return min(max(p, 0), (int)a.n_cap - 1);
-  };
+  // Key slot lane % 16 of step s (a key behind the list: its last). Its list entry is fetched
+  // kAhead steps before the step is copied and only looked at then: selecting or clamping it
+  // at once would wait for a load that may miss all the way to HBM.
+  constexpr int kAhead = 2;
+  auto at = [&](int s) { return min(s * kQ8Keys + (lane & 15), n_keys - 1); };
+  auto entry = [&](int s) -> int32_t { return __ldg(ib + min(max(at(s) - ni, 0), (int)kl.idx_stride - 1)); };
   const uint32_t ring = smem_u32(q8sm) + warp * (kQ8Stages * q8_stage_bytes<D>());
   auto issue = [&](int pos, uint32_t st) {
 #pragma unroll
@@ -247,18 +248,25 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][nt][e] = 0.f;
 
-  int pos_n = 0, s_n = s_beg;            // the next step to issue, and its positions
+  int s_n = s_beg;                       // the next step to issue
+  int32_t raw[kAhead];                   // list entries of steps s_n, s_n + s_inc, ...
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) raw[u] = entry(s_n + u * s_inc);
   uint32_t st_n = ring;                  // and the ring slot it goes to
   const uint32_t ring_end = ring + kQ8Stages * q8_stage_bytes<D>();
   auto advance = [&](uint32_t st) { return st + q8_stage_bytes<D>() == ring_end ? ring : st + q8_stage_bytes<D>(); };
   auto issue_next = [&]() {
-    if (s_n < s_end) issue(pos_n, st_n);
+    if (s_n < s_end) {
+      const int t = at(s_n), p = t < ni ? t : (t < ni + cnt ? raw[0] : t + jump);
+      issue(min(max(p, 0), (int)a.n_cap - 1), st_n);
+    }
     cp_async_commit();                   // one group per step, empty past the end
-    s_n += kw;
+#pragma unroll
+    for (int u = 0; u + 1 < kAhead; ++u) raw[u] = raw[u + 1];
+    raw[kAhead - 1] = entry(s_n + kAhead * s_inc);
+    s_n += s_inc;
     st_n = advance(st_n);
-    if (s_n < s_end) pos_n = position(s_n);
   };
-  if (s_n < s_end) pos_n = position(s_n);
 #pragma unroll
   for (int i = 0; i < kQ8Stages - 1; ++i) issue_next();
 
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   }
 
   uint32_t st = ring;
-  for (int s = s_beg; s < s_end; s += kw, st = advance(st)) {
+  for (int s = s_beg; s < s_end; s += s_inc, st = advance(st)) {
     cp_async_wait<kQ8Stages - 2>();      // this lane's pieces of step s are here
     __syncwarp();                        // every lane's are, and every lane has left the slot filled next
     issue_next();

@@ -19,11 +19,11 @@
 // tile's largest at worst; three int8 digits, 2^-21, showed in dims where the largest
 // weight's value is next to zero), and nothing in TMEM is ever rescaled.
 //
-// Roles (7 warps): warps 0-3 softmax (thread = key for S and W, thread = dim for O), warp 4
-// issues the MMAs, warps 5-6 copy keys, values and scales (16-byte cp.async, 8 lanes a
-// row, into 128-byte-swizzled tiles). TMEM: S and O, two buffers each. A CTA takes a share
-// of one (sequence, KV head)'s key list; the CTAs of a cluster meet in distributed shared
-// memory at the end.
+// Roles: one to three softmax warpgroups of up to 8 query rows each (thread = key for S and
+// W, thread = dim for O), one warp that issues the MMAs, two that copy keys, values and
+// scales (16-byte cp.async, 8 lanes a row, into 128-byte-swizzled tiles). TMEM: S and O, two
+// buffers each. A CTA takes a share of one (sequence, KV head)'s key list; at the end each
+// CTA of a cluster sends every other its part of their dims and merges its own.
 #pragma once
 #include "attn_q8.cuh"
 #include "common.cuh"
@@ -31,20 +31,30 @@
 
 namespace esa {
 
-constexpr int kQtThreads = 7 * 32;
 constexpr int kQtKeys = 128;
 constexpr uint32_t kQtTile = 128 * 128;                       // bytes of a key or value tile
 constexpr uint32_t kQtStage = 2 * kQtTile + 2 * kQtKeys * 4;  // keys, values, their scales
+constexpr int kQtMaxCluster = 8;
 
-template <int FMT, int RT>
+// WR query rows per softmax warpgroup, NWG warpgroups: RT rows of a tile.
+template <int FMT, int WR, int NWG>
 struct QtShape {
+  static constexpr int RT = WR * NWG;
   static constexpr int NQ = FMT == kQ8E4M3 ? 2 : 3, NW = FMT == kQ8E4M3 ? 3 : 4;   // pieces of a query, of a weight
   static constexpr int N = (NW * RT + 15) / 16 * 16;          // MMA columns (M = 128: a multiple of 16)
+  static constexpr int kThreads = (4 * NWG + 3) * 32;
   static constexpr int kCtas = RT <= 4 ? 2 : 1;               // per SM
   static constexpr int kStages = kCtas == 2 ? 3 : 5;
-  static constexpr uint32_t kCols = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 256;   // TMEM columns
+  static constexpr uint32_t kCols = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;   // TMEM columns
   static constexpr uint32_t kQ = kStages * kQtStage, kW = kQ + N * 128, kCtrl = kW + 2 * N * 128;
-  static constexpr uint32_t kSmem = kCtrl + 1024 + (2 * 4 * RT + 2 * RT + 4 * RT) * 4;
+  // behind the control block, in floats: tile maxima [2][4][RT], l of each warp [4][RT] (at
+  // first the logit factors [RT]), and what the cluster's CTAs send: (m, l) [8][RT][2], o
+  // [RT][128] (128 / csize dims of each CTA)
+  static constexpr int kMax = 0, kL = 8 * RT, kMl = 12 * RT, kO = kMl + 2 * kQtMaxCluster * RT;
+  static constexpr int kOFloats = 160 * RT;                   // csize * q8_dims_per(csize) <= 160
+  static constexpr uint32_t kRing = kCtrl + 256 + (kO + kOFloats) * 4;   // list entries [stage][128]
+  static constexpr uint32_t kSmem = kRing + kStages * 512;
+  static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024 && 4 * N * kCtas <= 512, "does not fit an SM");
 };
 
 struct QtCtrl {
@@ -52,7 +62,7 @@ struct QtCtrl {
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(QtCtrl) <= 1024, "control block overflows its reservation");
+static_assert(sizeof(QtCtrl) <= 256, "control block overflows its reservation");
 
 template <int FMT>
 __device__ __forceinline__ void umma_q8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -89,32 +99,35 @@ __device__ __forceinline__ float redux_max(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// N columns of a TMEM buffer, this thread's lane
-template <int N>
-__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t* v) {
+// NP pieces of WR columns, RT columns apart, of a TMEM buffer (this thread's lane)
+template <int NP, int WR, int RT>
+__device__ __forceinline__ void tmem_ld_pieces(uint32_t addr, uint32_t (&v)[NP * WR]) {
 #pragma unroll
-  for (int c = 0; c < N; c += 16)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[c]), "=r"(v[c + 1]), "=r"(v[c + 2]), "=r"(v[c + 3]), "=r"(v[c + 4]), "=r"(v[c + 5]), "=r"(v[c + 6]),
-          "=r"(v[c + 7]), "=r"(v[c + 8]), "=r"(v[c + 9]), "=r"(v[c + 10]), "=r"(v[c + 11]), "=r"(v[c + 12]),
-          "=r"(v[c + 13]), "=r"(v[c + 14]), "=r"(v[c + 15])
-        : "r"(addr + c));
+  for (int p = 0; p < NP; ++p) {
+    if constexpr (WR == 8)
+      tmem_ld8(addr + p * RT, v + p * 8);
+    else
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v[4 * p]), "=r"(v[4 * p + 1]), "=r"(v[4 * p + 2]), "=r"(v[4 * p + 3])
+                   : "r"(addr + p * RT));
+  }
   tmem_wait_ld();
 }
-// a row's value from its columns (NP pieces RT columns apart)
-template <int FMT, int RT, int NP>
+__device__ __forceinline__ void st_dsmem_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// a row's value from its pieces (v[p * WR + r])
+template <int FMT, int WR, int NP>
 __device__ __forceinline__ float q8_join(const uint32_t* v, int r) {
   if constexpr (FMT == kQ8E4M3) {
-    float x = __uint_as_float(v[(NP - 1) * RT + r]);
+    float x = __uint_as_float(v[(NP - 1) * WR + r]);
 #pragma unroll
-    for (int p = NP - 2; p >= 0; --p) x = fmaf(x, 0.0625f, __uint_as_float(v[p * RT + r]));
+    for (int p = NP - 2; p >= 0; --p) x = fmaf(x, 0.0625f, __uint_as_float(v[p * WR + r]));
     return x;
   } else {
-    float x = (float)(int)v[(NP - 1) * RT + r];
+    float x = (float)(int)v[(NP - 1) * WR + r];
 #pragma unroll
-    for (int p = NP - 2; p >= 0; --p) x = fmaf(x, 0.0078125f, (float)(int)v[p * RT + r]);
+    for (int p = NP - 2; p >= 0; --p) x = fmaf(x, 0.0078125f, (float)(int)v[p * WR + r]);
     return x;
   }
 }
@@ -145,79 +158,51 @@ __device__ __forceinline__ void q8_split2(float x0, float x1, uint32_t* pc) {
   }
 }
 
-// The CTAs of a cluster hold partial rows o [nrow][RF] with (m, l) pairs ml [nrow][2] at the
-// same shared-memory offsets; CTA `rank` writes its share of the merged rows. o carries a
-// factor 1 / o_scale; row r belongs to query (r0 + r) / G, head g * G + (r0 + r) % G.
-template <typename T, int RF, int D>
-__device__ __forceinline__ void q8_cluster_merge(const AttnQ8Args& a, const float* sm_o, const float* sm_ml, int b,
-                                                 int g, int r0, int nrow, int rank, int csize, float o_scale,
-                                                 int threads) {
-  constexpr int Q = D / 4;
-  for (int it = threadIdx.x + threads * rank; it < nrow * Q; it += threads * csize) {
-    const int d4 = it % Q, r = it / Q;
-    const uint32_t ml = smem_u32(sm_ml + r * 2), oo = smem_u32(sm_o + r * RF + d4 * 4);
-    float M = -INFINITY;
-    for (int u = 0; u < csize; ++u) M = fmaxf(M, __uint_as_float(ld_dsmem_u32(dsmem_map(ml, u))));
-    const float mr = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int u = 0; u < csize; ++u) {
-      const uint2 z = ld_dsmem_u2(dsmem_map(ml, u));
-      const float4 o = ld_dsmem_f4(dsmem_map(oo, u));
-      const float c = fast_exp2(__uint_as_float(z.x) - mr);
-      L += __uint_as_float(z.y) * c;
-      O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
-    }
-    const int i = (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
-    const int64_t row = ((int64_t)b * a.lq + i) * a.hq + g * a.G + hl;
-    const float inv = o_scale / L;
-    T* dst = static_cast<T*>(a.o) + row * D + d4 * 4;
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(dst) = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-    } else {
-      uint2 w;
-      w.x = bf16x2_rn(O.x * inv, O.y * inv);
-      w.y = bf16x2_rn(O.z * inv, O.w * inv);
-      *reinterpret_cast<uint2*>(dst) = w;
-    }
-    if (d4 == 0 && a.lse) a.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;
-  }
-}
+// Dims that each CTA of a cluster merges, a multiple of 4 (the last CTA the rest, if any).
+__device__ __forceinline__ int q8_dims_per(int csize) { return ((128 + csize - 1) / csize + 3) & ~3; }
 
-// grid (cluster size, Hkv * tiles, B), cluster (cluster size, 1, 1); a.hc = 1. RT: query
-// rows of a tile.
-template <int FMT, int RT>
-__global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8_tc_kernel(const AttnQ8Args a) {
-  using Sh = QtShape<FMT, RT>;
-  constexpr int N = Sh::N, NST = Sh::kStages, NQ = Sh::NQ, NW = Sh::NW;
+// grid (cluster size, Hkv * tiles, B), cluster (cluster size, 1, 1); a.hc = 1.
+template <int FMT, int WR, int NWG>
+__global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FMT, WR, NWG>::kCtas))
+    attn_q8_tc_kernel(const AttnQ8Args a) {
+  using Sh = QtShape<FMT, WR, NWG>;
+  constexpr int RT = Sh::RT, N = Sh::N, NST = Sh::kStages, NQ = Sh::NQ, NW = Sh::NW;
+  constexpr int kMmaWarp = 4 * NWG, kProdWarp = kMmaWarp + 1, kSoftThreads = 128 * NWG;
   // a weight of 1 (its tile's largest) goes in as 2^8 (e4m3, <= 448), 2^27 (int8, <= 127 * 2^21)
   constexpr float kTop = FMT == kQ8E4M3 ? 8.f : 27.f;
   // units of the first piece of a query and of a weight
   constexpr float kUnitQ = FMT == kQ8E4M3 ? 1.f : 0x1p14f, kUnitW = FMT == kQ8E4M3 ? 1.f : 0x1p21f;
-  constexpr int RF = 132;
   extern __shared__ __align__(1024) uint8_t qtsm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(qtsm);
   QtCtrl& sm = *reinterpret_cast<QtCtrl*>(qtsm + Sh::kCtrl);
-  float* const sm_max = reinterpret_cast<float*>(qtsm + Sh::kCtrl + 1024);   // [2][4 warps][RT] tile maxima
-  float* const sm_ml = sm_max + 8 * RT;                                      // [RT][2]
-  float* const sm_l = sm_ml + 2 * RT;                                        // [4 warps][RT]
-  float* const sm_o = reinterpret_cast<float*>(qtsm);                        // [RT][RF], over the stages at the end
+  float* const smf = reinterpret_cast<float*>(qtsm + Sh::kCtrl + 256);
+  float* const sm_l = smf + Sh::kL;
 
   const int g = blockIdx.y / a.tiles, tile = blockIdx.y - g * a.tiles, b = blockIdx.z;
   const int rank = blockIdx.x, csize = gridDim.x;
   const int list = a.lists > 1 ? b * a.lists + g : b;
   KeyList kl = a.keys;
   const int64_t c0 = kl.vl.len ? kl.resolve(b, 706) : a.c0;
-  const int cnt = min(max(kl.count[list], 0), (int)kl.idx_stride);
-  const int n_prior = (int)(kl.ni + cnt + (c0 - kl.lo));
-  const int r0 = tile * RT, nrow = min(RT, a.lq * a.G - r0);
-  const int n_keys = n_prior + (r0 + nrow - 1) / a.G + 1;      // that the tile's last row attends
-  const int n_all = n_prior + r0 / a.G + 1;                    // that every row of the tile attends
-  const int tiles_all = (n_keys + kQtKeys - 1) / kQtKeys;
-  const int j0 = (int)((int64_t)tiles_all * rank / csize);
-  const int nt = (int)((int64_t)tiles_all * (rank + 1) / csize) - j0;   // this CTA's key tiles
-
+  const int ni = (int)kl.ni;
+  // Key slot `row` of tile j of this CTA (tiles rank, rank + csize, ...: every CTA gets its
+  // share of the scattered keys, which load slower than the consecutive ones: with
+  // consecutive shares the CTA of the local tokens waited 11 of 45 us for its peer), and the
+  // place of its list entry, if it has one. Entries (loads that may miss all the way to HBM)
+  // do not wait for the list's length.
+  auto slot_t = [&](int j, int row) { return (j * csize + rank) * kQtKeys + row; };
+  auto entry = [&](int j, int row) {
+    return kl.idx + (int64_t)list * kl.idx_stride + min(max(slot_t(j, row) - ni, 0), (int)kl.idx_stride - 1);
+  };
+  const int prow = (warp - kProdWarp) * 64 + lane;  // producer lanes: rows prow and prow + 32 of a tile
+  int32_t raw[NST][2];
+  if (warp >= kProdWarp) {
+#pragma unroll
+    for (int u = 0; u < NST; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) raw[u][h] = __ldg(entry(u, prow + 32 * h));
+  }
+  const int32_t n_listed = kl.count[list];
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&sm.full[s], 64);                   // every producer thread, when its copies have landed
@@ -225,58 +210,81 @@ __global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.w_full[s], 4);
+      mbar_init(&sm.w_full[s], 4 * NWG);
       mbar_init(&sm.o_full[s], 1);
     }
-    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.q_full, 4 * NWG);
     mbar_init(&sm.mma_done, 1);
     sm.abort_flag = base & 1023u ? 1 : 0;
     if (base & 1023u) record_status(5u, 710);
     fence_barrier_init();
   }
-  if (warp == 4) {
-    tmem_alloc(&sm.tmem_base, Sh::kCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  if (csize > 1) cluster_arrive();                  // this CTA runs: its shared memory may be written to
+  const int cnt = min(max(n_listed, 0), (int)kl.idx_stride);
+  const int n_prior = (int)(kl.ni + cnt + (c0 - kl.lo));
+  const int r0 = tile * RT, nrow = min(RT, a.lq * a.G - r0);
+  const int n_keys = n_prior + (r0 + nrow - 1) / a.G + 1;      // that the tile's last row attends
+  const int n_all = n_prior + r0 / a.G + 1;                    // that every row of the tile attends
+  const int tiles_all = (n_keys + kQtKeys - 1) / kQtKeys;
+  const int nt = rank < tiles_all ? (tiles_all - rank - 1) / csize + 1 : 0;   // this CTA's key tiles
   volatile int* abort_flag = &sm.abort_flag;
+  // TMEM is the softmax and MMA warps' business: the producers are off already
+  uint32_t tmem = 0;
+  if (warp <= kMmaWarp) {
+    if (warp == kMmaWarp) {
+      tmem_alloc(&sm.tmem_base, Sh::kCols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    asm volatile("bar.sync %0, %1;" ::"n"(NWG + 1), "n"(kSoftThreads + 32) : "memory");
+    tc_fence_after();
+    tmem = sm.tmem_base;
+  }
 
-  float o[RT], m[RT], l[RT];
+  float o[WR], m[WR], l[WR];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
+  for (int r = 0; r < WR; ++r) {
     o[r] = 0.f;
     m[r] = -INFINITY;
     l[r] = 0.f;
   }
 
-  if (*abort_flag) {
+  if (base & 1023u) {
     // misaligned shared memory: reported, nothing done
-  } else if (warp >= 5) {
+    if (csize > 1 && warp < kMmaWarp) cluster_wait();
+  } else if (warp >= kProdWarp) {
     // ------------------------------------------------------------------- producers
     const uint32_t row_bytes = (uint32_t)a.hkv * 128;
-    const int pw = warp - 5, c = lane & 7, lr = lane >> 3;
+    const int pw = warp - kProdWarp, c = lane & 7, lr = lane >> 3;
     const uint8_t* kb = a.k + (int64_t)b * a.n_cap * row_bytes + g * 128 + c * 16;
     const uint8_t* vb = a.v + (int64_t)b * a.n_cap * row_bytes + g * 128 + c * 16;
     const float* ksb = a.ks + (int64_t)b * a.nblk * a.hkv + g;
     const float* vsb = a.vs + (int64_t)b * a.nblk * a.hkv + g;
-    const int32_t* ib = kl.idx + (int64_t)list * kl.idx_stride;
-    const int ni = (int)kl.ni, jump = (int)(kl.lo - kl.ni) - cnt;
-    auto position = [&](int j, int h) -> int {      // of row 64 pw + 32 h + lane (behind the list: its last key)
-      const int t = min((j0 + j) * kQtKeys + pw * 64 + h * 32 + lane, n_keys - 1);
-      const int p = t < ni ? t : (t < ni + cnt ? __ldg(ib + t - ni) : t + jump);
-      return min(max(p, 0), (int)a.n_cap - 1);
-    };
-    int pos[2] = {0, 0};
-    if (nt > 0) { pos[0] = position(0, 0); pos[1] = position(0, 1); }
+    const int jump = (int)(kl.lo - kl.ni) - cnt;
+    // Later entries are copied a ring ahead, with tile j - NST, into shared memory, where each
+    // lane reads back its own: the stage of tile j is free only after those copies have landed.
+    const uint32_t ring = base + Sh::kRing + prow * 4;
+#pragma unroll
+    for (int u = 0; u < NST; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + u * 512 + h * 128), "r"(raw[u][h]) : "memory");
     const uint32_t sw0 = (uint32_t)(pw * 64 + lr) * 128 + ((c ^ lr) << 4);            // rows 8 i + lr
     const uint32_t sw1 = (uint32_t)(pw * 64 + 4 + lr) * 128 + ((c ^ (4 + lr)) << 4);  // rows 8 i + 4 + lr
-    for (int j = 0; j < nt; ++j) {
-      const int s = j % NST;
+    int s = 0;
+    for (int j = 0; j < nt; ++j, s = s + 1 == NST ? 0 : s + 1) {
       if (!mbar_wait_warp(&sm.empty[s], ((j / NST) & 1) ^ 1, abort_flag, 707)) break;
       const uint32_t kd = base + s * kQtStage, vd = kd + kQtTile;
+      int pos[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = min(slot_t(j, prow + 32 * h), n_keys - 1);             // behind the list: its last key
+        const int e = (int)lds32(ring + s * 512 + h * 128);
+        const int p = t < ni ? t : (t < ni + cnt ? e : t + jump);
+        pos[h] = min(max(p, 0), (int)a.n_cap - 1);
+        cp_async4(ring + s * 512 + h * 128, entry(j + NST, prow + 32 * h));
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -294,39 +302,51 @@ __global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8
         cp_async4(d + kQtKeys * 4, vsb + so);
       }
       cp_async_arrive(&sm.full[s]);
-      if (j + 1 < nt) { pos[0] = position(j + 1, 0); pos[1] = position(j + 1, 1); }
     }
     cp_async_wait_all();
-  } else if (warp == 4) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_s = q8_idesc<FMT>(N, 0), idesc_o = q8_idesc<FMT>(N, 1);
       const uint64_t dq = sdesc_sw128(base + Sh::kQ, 16, 1024);
-      // S_j into buffer j & 1: its previous scores S_{j-2} were read before w_full[j - 2]
-      auto issue_s = [&](int j) -> bool {
-        const int s = j % NST;
-        if (!mbar_wait(&sm.full[s], (j / NST) & 1, abort_flag, 708)) return false;
-        fence_proxy_async();                        // cp.async wrote through the generic proxy
-        tc_fence_after();
-        const uint64_t dk = sdesc_sw128(base + s * kQtStage, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_q8<FMT>(tmem + (j & 1) * N, dk + kk * 2, dq + kk * 2, idesc_s, kk > 0);
-        umma_commit(&sm.s_full[j & 1]);
-        return true;
-      };
       bool ok = nt == 0 || mbar_wait(&sm.q_full, 0, abort_flag, 709);
-      for (int j = 0; j < 2 && j < nt && ok; ++j) ok = issue_s(j);
-      for (int j = 0; j < nt && ok; ++j) {
-        if (!(ok = mbar_wait(&sm.w_full[j & 1], (j >> 1) & 1, abort_flag, 711))) break;
-        tc_fence_after();
-        const uint64_t dv = sdesc_sw128(base + (j % NST) * kQtStage + kQtTile, 16, 1024);
-        const uint64_t dw = sdesc_sw128(base + Sh::kW + (j & 1) * N * 128, 16, 1024);
+      // Whichever is ready next: S of tile js (its codes have landed, and js < jp + 2: the
+      // scores that were in its buffer have been read, as w_full[js - 2] says), or O of tile
+      // jp (its weights are written). Waiting for the two in a fixed order held O_j, and
+      // with it the release of a stage, until tile j + 1 had landed.
+      int js = 0, jp = 0;
+      uint64_t since = globaltimer_ns();
+      for (uint32_t spin = 0; ok && jp < nt;) {
+        if (jp < js && mbar_test_wait(&sm.w_full[jp & 1], (jp >> 1) & 1)) {
+          tc_fence_after();
+          const uint64_t dv = sdesc_sw128(base + (jp % NST) * kQtStage + kQtTile, 16, 1024);
+          const uint64_t dw = sdesc_sw128(base + Sh::kW + (jp & 1) * N * 128, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)              // 32 keys: four 8-row groups of V, 32 bytes of a W row
-          umma_q8<FMT>(tmem + (2 + (j & 1)) * N, dv + kk * 256, dw + kk * 2, idesc_o, kk > 0);
-        umma_commit(&sm.o_full[j & 1]);
-        umma_commit(&sm.empty[j % NST]);
-        if (j + 2 < nt) ok = issue_s(j + 2);
+          for (int kk = 0; kk < 4; ++kk)            // 32 keys: four 8-row groups of V, 32 bytes of a W row
+            umma_q8<FMT>(tmem + (2 + (jp & 1)) * N, dv + kk * 256, dw + kk * 2, idesc_o, kk > 0);
+          umma_commit(&sm.o_full[jp & 1]);
+          umma_commit(&sm.empty[jp % NST]);
+          ++jp;
+          spin = 0;
+        } else if (js < nt && js < jp + 2 && mbar_test_wait(&sm.full[js % NST], (js / NST) & 1)) {
+          fence_proxy_async();                      // cp.async wrote through the generic proxy
+          tc_fence_after();
+          const uint64_t dk = sdesc_sw128(base + (js % NST) * kQtStage, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_q8<FMT>(tmem + (js & 1) * N, dk + kk * 2, dq + kk * 2, idesc_s, kk > 0);
+          umma_commit(&sm.s_full[js & 1]);
+          ++js;
+          spin = 0;
+        } else if (spin++ == 0) {
+          since = globaltimer_ns();
+        } else if ((spin & 255u) == 0) {
+          if (*abort_flag) ok = false;
+          else if (globaltimer_ns() - since > ESA_WAIT_LIMIT_NS) {
+            *abort_flag = 1;
+            record_status(4u, 708);
+            ok = false;
+          }
+        }
       }
       // every MMA issued so far has completed before TMEM and shared memory are reused
       umma_commit(&sm.mma_done);
@@ -335,11 +355,14 @@ __global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8
     __syncwarp();
   } else {
     // ------------------------------------------------------------------- softmax warps
-    // queries as pieces: thread (r, part) takes 128 / (128 / RT) dims of row r
-    constexpr int TPR = 128 / RT, DPT = 128 / TPR;  // threads of a row, dims of a thread
-    float xs[RT];                                   // logit factor of each row
+    const int wg = NWG == 1 ? 0 : warp >> 2, key = threadIdx.x & 127;    // key of a tile, for S and W; the dim, for O
+    const uint32_t bar_wg = 1 + wg;                       // named barrier of the warpgroup
+    const int row_wg = wg * WR;                           // its first row of the tile
+    // queries as pieces: thread (r, part) takes DPT dims of row r
+    constexpr int TPR = 128 / WR, DPT = 128 / TPR;
+    float xs[WR];                                   // logit factor of each row
     {
-      const int r = threadIdx.x / TPR, part = threadIdx.x % TPR;
+      const int r = row_wg + key / TPR, part = key % TPR;
       const int rr = min(r0 + r, a.lq * a.G - 1), i = rr / a.G, hl = rr - i * a.G;
       const __nv_bfloat16* qp =
           static_cast<const __nv_bfloat16*>(a.q) + (((int64_t)b * a.lq + i) * a.hq + g * a.G + hl) * 128 + part * DPT;
@@ -375,77 +398,75 @@ __global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8
       // columns that belong to no piece: zero in the queries and in both weight buffers
       if constexpr (N > NW * RT) {
         constexpr int pad = (N - NW * RT) * 8;          // 16-byte pieces of a buffer (W follows Q)
-        for (int z = threadIdx.x; z < 3 * pad; z += 128)
+        for (int z = threadIdx.x; z < 3 * pad; z += kSoftThreads)
           st_shared_v4(base + Sh::kQ + ((z / pad) * N + NW * RT) * 128 + (z % pad) * 16, 0u, 0u, 0u, 0u);
       }
       fence_proxy_async();
       mbar_arrive_warp(&sm.q_full);
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync %0, 128;" ::"r"(bar_wg) : "memory");
 #pragma unroll
-      for (int q = 0; q < RT; ++q) xs[q] = sm_l[q];
+      for (int q = 0; q < WR; ++q) xs[q] = sm_l[row_wg + q];
     }
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const int key = threadIdx.x;                    // of a tile, for S and W; the dim, for O
-    float al[RT], be[RT];                           // the tile's factors on o and on its own O
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + row_wg;
+    float al[WR], be[WR];                           // the tile's factors on o and on its own O
     auto drain = [&](int j) -> bool {               // o = o al + O_j be
       if (!mbar_wait_warp(&sm.o_full[j & 1], (j >> 1) & 1, abort_flag, 712)) return false;
       tc_fence_after();
-      uint32_t v[N];
-      tmem_ld_n<N>(lane_base + (2 + (j & 1)) * N, v);
+      uint32_t v[NW * WR];
+      tmem_ld_pieces<NW, WR, RT>(lane_base + (2 + (j & 1)) * N, v);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) o[r] = fmaf(o[r], al[r], q8_join<FMT, RT, NW>(v, r) * be[r]);
+      for (int r = 0; r < WR; ++r) o[r] = fmaf(o[r], al[r], q8_join<FMT, WR, NW>(v, r) * be[r]);
       return true;
     };
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
       // (full: the scales, which this warp reads itself)
-      ok = ok && mbar_wait_warp(&sm.full[j % NST], (j / NST) & 1, abort_flag, 715) &&
-           mbar_wait_warp(&sm.s_full[j & 1], (j >> 1) & 1, abort_flag, 713);
-      // a named barrier has no time limit: all four warps leave together
-      if (!(ok = bar_all(1, 128, ok))) break;
+      ok = ok && mbar_wait_warp(&sm.s_full[j & 1], (j >> 1) & 1, abort_flag, 713) &&
+           mbar_wait_warp(&sm.full[j % NST], (j / NST) & 1, abort_flag, 715);
       tc_fence_after();
-      float x[RT];
+      float x[WR];
       const float* sc = reinterpret_cast<const float*>(qtsm + (j % NST) * kQtStage + 2 * kQtTile);
       const float ka = sc[key];
       const float lv = __log2f(fmaxf(sc[kQtKeys + key], 0x1p-120f));
       {
-        uint32_t v[N];
-        tmem_ld_n<N>(lane_base + (j & 1) * N, v);
+        uint32_t v[NQ * WR];
+        tmem_ld_pieces<NQ, WR, RT>(lane_base + (j & 1) * N, v);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) x[r] = fmaf(q8_join<FMT, RT, NQ>(v, r), ka * xs[r], lv);
+        for (int r = 0; r < WR; ++r) x[r] = fmaf(q8_join<FMT, WR, NQ>(v, r), ka * xs[r], lv);
       }
-      const int t0 = (j0 + j) * kQtKeys;
+      const int t0 = slot_t(j, 0);
       if (t0 + kQtKeys > n_all) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-          if (t0 + key >= n_prior + min(r0 + r, a.lq * a.G - 1) / a.G + 1) x[r] = -INFINITY;
+        for (int r = 0; r < WR; ++r)
+          if (t0 + key >= n_prior + min(r0 + row_wg + r, a.lq * a.G - 1) / a.G + 1) x[r] = -INFINITY;
       }
       // the tile's maximum of each row
-      float mt[RT];
-      float* mx = sm_max + (j & 1) * 4 * RT;
+      float mt[WR];
+      float* mx = smf + Sh::kMax + (j & 1) * 4 * RT + row_wg;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int r = 0; r < WR; ++r) {
         mt[r] = redux_max(x[r]);
-        if (lane == 0) mx[warp * RT + r] = mt[r];
+        if (lane == 0) mx[(warp & 3) * RT + r] = mt[r];
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // a named barrier has no time limit: the four warps leave together if a wait ran out
+      if (!(ok = bar_all(bar_wg, 128, ok))) break;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int r = 0; r < WR; ++r)
         mt[r] = fmaxf(fmaxf(mx[r], mx[RT + r]), fmaxf(mx[2 * RT + r], mx[3 * RT + r]));
       // weights, as pieces, to row p * RT + r of the W buffer, byte `key`
-      const uint32_t wb = base + Sh::kW + (j & 1) * N * 128;
+      const uint32_t wb = base + Sh::kW + (j & 1) * N * 128 + row_wg * 128 + (key & 15);
       const float iv = fast_exp2(-lv - kTop);
 #pragma unroll
-      for (int r = 0; r < RT; r += 2) {
+      for (int r = 0; r < WR; r += 2) {
         uint32_t pc[NW];
         x[r] = fast_exp2(x[r] - (mt[r] == -INFINITY ? 0.f : mt[r]) + kTop);
         x[r + 1] = fast_exp2(x[r + 1] - (mt[r + 1] == -INFINITY ? 0.f : mt[r + 1]) + kTop);
         q8_split2<FMT, NW>(x[r], x[r + 1], pc);
 #pragma unroll
         for (int p = 0; p < NW; ++p) {
-          const uint32_t n0 = p * RT + r, n1 = n0 + 1;
-          st_shared_u8(wb + n0 * 128 + (((key >> 4) ^ (n0 & 7)) << 4) + (key & 15), pc[p]);
-          st_shared_u8(wb + n1 * 128 + (((key >> 4) ^ (n1 & 7)) << 4) + (key & 15), pc[p] >> 8);
+          const uint32_t n0 = p * RT + r, n1 = n0 + 1;           // (row_wg is a multiple of 8, or 0)
+          st_shared_u8(wb + n0 * 128 + (((key >> 4) ^ (n0 & 7)) << 4), pc[p]);
+          st_shared_u8(wb + n1 * 128 + (((key >> 4) ^ (n1 & 7)) << 4), pc[p] >> 8);
         }
       }
       fence_proxy_async();
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8
       mbar_arrive_warp(&sm.w_full[j & 1]);
       if (j > 0) ok = drain(j - 1);                 // (a wait that ran out: the next bar_all)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int r = 0; r < WR; ++r) {
         const float mn = fmaxf(m[r], mt[r]);
         const float mr = mn == -INFINITY ? 0.f : mn;
         al[r] = fast_exp2(m[r] - mr);
@@ -464,30 +485,65 @@ __global__ void __launch_bounds__(kQtThreads, (QtShape<FMT, RT>::kCtas)) attn_q8
       }
     }
     if (nt > 0 && ok) ok = drain(nt - 1);
-  }
-  tc_fence_before();
-  __syncthreads();                                  // every MMA and copy is done: the stages are free
-  tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, Sh::kCols);
-  if (warp < 4) {
+
+    // ---- the CTA's row sums, then every CTA of the cluster gets its share of the dims (dim
+    // d belongs to CTA d / per) and all (m, l)
+    asm volatile("bar.sync %0, 128;" ::"r"(bar_wg) : "memory");      // (xs have been read)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      sm_o[r * RF + threadIdx.x] = o[r];
+    for (int r = 0; r < WR; ++r) {
       const float s = warp_sum(l[r]);
-      if (lane == 0) sm_l[warp * RT + r] = s;
-      if (threadIdx.x == 0) sm_ml[2 * r] = m[r];
+      if (lane == 0) sm_l[(warp & 3) * RT + row_wg + r] = s;
+    }
+    if (csize > 1) cluster_wait();
+    const int per = q8_dims_per(csize), owner = key / per, slot = key - owner * per;
+    const uint32_t my_o = smem_u32(smf + Sh::kO), my_ml = smem_u32(smf + Sh::kMl);
+    const uint32_t dst = dsmem_map(my_o, owner) + (rank * per + slot) * 4;
+#pragma unroll
+    for (int r = 0; r < WR; ++r) st_dsmem_f32(dst + (row_wg + r) * per * csize * 4, o[r]);
+    asm volatile("bar.sync %0, 128;" ::"r"(bar_wg) : "memory");
+    for (int it = key; it < WR * csize; it += 128) {
+      const int to = it / WR, r = row_wg + it % WR;
+      const float L = (sm_l[r] + sm_l[RT + r]) + (sm_l[2 * RT + r] + sm_l[3 * RT + r]);
+      const uint32_t p = dsmem_map(my_ml, to) + (rank * RT + r) * 8;
+      float mm = m[0];
+#pragma unroll
+      for (int q = 1; q < WR; ++q) mm = it % WR == q ? m[q] : mm;
+      st_dsmem_f32(p, mm);
+      st_dsmem_f32(p + 4, L);
     }
   }
+  if (csize > 1 && warp >= kMmaWarp) cluster_wait();
+  tc_fence_before();
   __syncthreads();
-  if (threadIdx.x < RT)
-    sm_ml[2 * threadIdx.x + 1] = (sm_l[threadIdx.x] + sm_l[RT + threadIdx.x]) +
-                                 (sm_l[2 * RT + threadIdx.x] + sm_l[3 * RT + threadIdx.x]);
-  if (csize > 1) cluster_sync_all();
-  else __syncthreads();
-  if (!*abort_flag)
-    q8_cluster_merge<__nv_bfloat16, RF, 128>(a, sm_o, sm_ml, b, g, r0, nrow, rank, csize,
-                                             FMT == kQ8E4M3 ? 0x1p-8f : 0x1p-27f, kQtThreads);
-  if (csize > 1) cluster_sync_all();                // no CTA leaves while it is read
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, Sh::kCols);
+  if (csize > 1) cluster_sync_all();                // every CTA's rows are here
+  if (*abort_flag) return;
+  const int per = q8_dims_per(csize), d0 = rank * per, d = lane * 4;
+  if (d >= min(per, 128 - d0)) return;
+  for (int r = warp; r < nrow; r += Sh::kThreads / 32) {         // a row per warp, four dims per lane
+    const float* ml = smf + Sh::kMl + r * 2;        // [csize][RT][2]
+    const float* po = smf + Sh::kO + r * per * csize + d;
+    float M = -INFINITY;
+    for (int u = 0; u < csize; ++u) M = fmaxf(M, ml[u * RT * 2]);
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < csize; ++u) {
+      const float2 z = *reinterpret_cast<const float2*>(ml + u * RT * 2);
+      const float4 x = *reinterpret_cast<const float4*>(po + u * per);
+      const float c = fast_exp2(z.x - (M == -INFINITY ? 0.f : M));
+      L += z.y * c;
+      O.x += x.x * c; O.y += x.y * c; O.z += x.z * c; O.w += x.w * c;
+    }
+    const int i = a.lq == 1 ? 0 : (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
+    const int64_t row = ((int64_t)b * a.lq + i) * a.hq + g * a.G + hl;
+    const float inv = (FMT == kQ8E4M3 ? 0x1p-8f : 0x1p-27f) / L;
+    uint2 w;
+    w.x = bf16x2_rn(O.x * inv, O.y * inv);
+    w.y = bf16x2_rn(O.z * inv, O.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * 128 + d0 + d) = w;
+    if (d0 + d == 0 && a.lse) a.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;
+  }
 }
 
 }  // namespace esa

@@ -1314,22 +1314,49 @@ esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int nt, dim3
                  : launch_attn_q8<T, D, esa::kQ8Int8, 2>(a, grid, csize, s);
 }
 
-template <int FMT, int RT>
+template <int FMT, int WR, int NWG>
 esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cudaStream_t s) {
-  using Sh = esa::QtShape<FMT, RT>;
+  using Sh = esa::QtShape<FMT, WR, NWG>;
   static const char what = 0;
   const esa_status_t st =
-      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_tc_kernel<FMT, RT>, Sh::kSmem); });
+      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_tc_kernel<FMT, WR, NWG>, Sh::kSmem); });
   if (st != ESA_OK) return st;
-  a.hc = 1;
-  a.tiles = (int)cdiv((int64_t)a.lq * a.G, RT);
-  const int64_t units = (int64_t)batch * a.hkv * a.tiles, slots = 148 * Sh::kCtas;
+  a.tiles = (int)cdiv((int64_t)a.lq * a.G, Sh::RT);
   if ((int64_t)a.hkv * a.tiles > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
-  const int csize =
-      (int)std::max<int64_t>(1, std::min<int64_t>({8, slots / units, cdiv(n_keys, esa::kQtKeys)}));
+  // How many clusters of 2 .. 8 CTAs fit the GPU at once (a byte each; the SMs of a GPC do not
+  // divide by every size: 24 clusters of 6 CTAs of one per SM left 8 CTAs to a second wave).
+  // The query counts one CTA of this kernel per SM; where shared memory, registers and TMEM
+  // are laid out for two, as many clusters again fit beside the first.
+  static const char fits = 0;
+  intptr_t fit = 0;
+  const esa_status_t qs = per_context(&fits, &fit, [](intptr_t* v) {
+    for (int c = 2; c <= esa::kQtMaxCluster; ++c) {
+      cudaLaunchConfig_t q = {};
+      q.gridDim = dim3(c);
+      q.blockDim = dim3(Sh::kThreads);
+      q.dynamicSmemBytes = Sh::kSmem;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = c;
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      q.attrs = at;
+      q.numAttrs = 1;
+      int n = 0;
+      ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, esa::attn_q8_tc_kernel<FMT, WR, NWG>, &q));
+      *v |= (intptr_t)std::min(n * Sh::kCtas, 255) << (8 * (c - 2));
+    }
+    return ESA_OK;
+  });
+  if (qs != ESA_OK) return qs;
+  // the largest cluster with which every unit of work still runs at once
+  const int64_t units = (int64_t)batch * a.hkv * a.tiles, tiles = cdiv(n_keys, esa::kQtKeys);
+  int csize = 1;
+  for (int c = 2; c <= esa::kQtMaxCluster && c <= tiles; ++c)
+    if (units <= ((fit >> (8 * (c - 2))) & 255)) csize = c;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(csize, a.hkv * a.tiles, batch);
-  cfg.blockDim = dim3(esa::kQtThreads);
+  cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -1339,16 +1366,18 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  ESA_CUDA(cudaLaunchKernelEx(&cfg, esa::attn_q8_tc_kernel<FMT, RT>, a));
+  ESA_CUDA(cudaLaunchKernelEx(&cfg, esa::attn_q8_tc_kernel<FMT, WR, NWG>, a));
   ESA_LAUNCH_CHECK("attn_q8_tc_kernel");
   return ok();
 }
+// Rows in as few equal tiles as 24 rows allow, and the warpgroups that hold such a tile.
 template <int FMT>
 esa_status_t dispatch_attn_q8_tc(const esa::AttnQ8Args& a, int32_t batch, int64_t n_keys, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.lq * a.G;
-  if (rows <= 4) return launch_attn_q8_tc<FMT, 4>(a, batch, n_keys, s);
-  if (rows <= 8) return launch_attn_q8_tc<FMT, 8>(a, batch, n_keys, s);
-  return launch_attn_q8_tc<FMT, 16>(a, batch, n_keys, s);
+  const int64_t rows = (int64_t)a.lq * a.G, rt = cdiv(rows, cdiv(rows, 24));
+  if (rt <= 4) return launch_attn_q8_tc<FMT, 4, 1>(a, batch, n_keys, s);
+  if (rt <= 8) return launch_attn_q8_tc<FMT, 8, 1>(a, batch, n_keys, s);
+  if (rt <= 16) return launch_attn_q8_tc<FMT, 8, 2>(a, batch, n_keys, s);
+  return launch_attn_q8_tc<FMT, 8, 3>(a, batch, n_keys, s);
 }
 
 // The chunk form: the key list dequantised into the workspace, then attn_tc_kernel.
