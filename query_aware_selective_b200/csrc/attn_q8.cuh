@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
 
   const int list = a.lists > 1 ? b * a.lists + g : b;
   KeyList kl = a.keys;
+  pdl_wait();
   const int64_t c0 = kl.vl.len ? kl.resolve(b, 704) : a.c0;
   const int cnt = min(max(kl.count[list], 0), (int)kl.idx_stride);
   const int n_prior = (int)(kl.ni + cnt + (c0 - kl.lo));       // keys before the first query's own

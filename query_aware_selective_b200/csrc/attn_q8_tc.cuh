@@ -183,6 +183,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
   const int rank = blockIdx.x, csize = gridDim.x;
   const int list = a.lists > 1 ? b * a.lists + g : b;
   KeyList kl = a.keys;
+  pdl_wait();
   const int64_t c0 = kl.vl.len ? kl.resolve(b, 706) : a.c0;
   const int ni = (int)kl.ni;
   // Key slot `row` of tile j of this CTA (tiles rank, rank + csize, ...: every CTA gets its

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
   constexpr int NP = 4;                            // rows of a thread
   const uint32_t width = 2u * a.hkv, yb = blockIdx.x / width, col = blockIdx.x - yb * width;
   const int op = col >= (uint32_t)a.hkv, h = col - (op ? a.hkv : 0), b = blockIdx.y;
+  pdl_wait();
   int64_t start, end;
   if (!q8_write_range(a, b, start, end)) return;
   const int64_t blk = (start >> a.bshift) + yb;
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const Cache
   const int tr = threadIdx.x / tile.cols, col = cc * kReadThreads + threadIdx.x - tr * tile.cols;
   if (tr >= tile.rows || col * N >= row_bytes) return;
   const int64_t row0 = (int64_t)rt * (tile.rows * kReadPer) + tr;
+  pdl_wait();
   int pos[kReadPer];
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_stage_q8_kernel(const Cach
   const int tr = threadIdx.x / tile.cols, col = cc * kReadThreads + threadIdx.x - tr * tile.cols;
   if (tr >= tile.rows || col * 16 >= row_bytes) return;
   const int64_t row0 = (int64_t)rt * (tile.rows * kReadPer) + tr;
+  pdl_wait();
   const int g = col >> 3, list = a.lists > 1 ? b * a.lists + g : b;
   const int cnt = min(max(a.keys.count[list], 0), (int)a.keys.idx_stride);
   const int64_t n_keys = a.keys.ni + cnt + (a.c0 - a.keys.lo) + a.lq;

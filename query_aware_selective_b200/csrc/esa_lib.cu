@@ -1188,10 +1188,38 @@ int log2_of(int x) {
   return n;
 }
 
+// Launch with programmatic dependent launch (every kernel launched so waits in pdl_wait
+// before it touches memory), in clusters of `cluster` CTAs along x.
+template <typename Args>
+esa_status_t launch_q8(void (*kernel)(Args), const char* what, dim3 grid, int threads, int smem, int cluster,
+                       cudaStream_t s, const Args& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(ESA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  }
+  return check_launch(what);
+}
+
 template <typename T, int D>
-void launch_write_q8(const esa::CacheWriteArgs& a, int format, dim3 grid, int threads, cudaStream_t s) {
-  if (format == ESA_Q8_E4M3) esa::cache_write_q8_kernel<T, D, esa::kQ8E4M3><<<grid, threads, 0, s>>>(a);
-  else esa::cache_write_q8_kernel<T, D, esa::kQ8Int8><<<grid, threads, 0, s>>>(a);
+esa_status_t launch_write_q8(const esa::CacheWriteArgs& a, int format, dim3 grid, int threads, cudaStream_t s) {
+  return launch_q8(format == ESA_Q8_E4M3 ? esa::cache_write_q8_kernel<T, D, esa::kQ8E4M3>
+                                         : esa::cache_write_q8_kernel<T, D, esa::kQ8Int8>,
+                   "cache_write_q8_kernel", grid, threads, 0, 1, s, a);
 }
 
 esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int64_t rows, int64_t kbs, int64_t krs,
@@ -1238,15 +1266,14 @@ esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int6
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (blocks * 2 * c.hkv >= ((int64_t)1 << 31)) return fail(ESA_ERR_UNSUPPORTED, "too many rows in one write");
   const dim3 grid((unsigned)(blocks * 2 * c.hkv), c.batch);
-  if (dt == ESA_BF16) {
-    if (c.head_dim == 128) launch_write_q8<__nv_bfloat16, 128>(a, c.format, grid, threads, s);
-    else launch_write_q8<__nv_bfloat16, 64>(a, c.format, grid, threads, s);
-  } else {
-    if (c.head_dim == 128) launch_write_q8<float, 128>(a, c.format, grid, threads, s);
-    else launch_write_q8<float, 64>(a, c.format, grid, threads, s);
-  }
-  ESA_LAUNCH_CHECK("cache_write_q8_kernel");
-  return ok();
+  esa_status_t ls;
+  if (dt == ESA_BF16)
+    ls = c.head_dim == 128 ? launch_write_q8<__nv_bfloat16, 128>(a, c.format, grid, threads, s)
+                           : launch_write_q8<__nv_bfloat16, 64>(a, c.format, grid, threads, s);
+  else
+    ls = c.head_dim == 128 ? launch_write_q8<float, 128>(a, c.format, grid, threads, s)
+                           : launch_write_q8<float, 64>(a, c.format, grid, threads, s);
+  return ls == ESA_OK ? ok() : ls;
 }
 
 bool q8_tensor_cores(int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
@@ -1289,21 +1316,9 @@ esa_status_t launch_attn_q8(const esa::AttnQ8Args& a, dim3 grid, int csize, cuda
   const esa_status_t st =
       once_per_context(&what, [] { return set_max_smem(esa::attn_q8_kernel<T, D, FMT, NT>, smem); });
   if (st != ESA_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(esa::kQ8Threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = csize;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  ESA_CUDA(cudaLaunchKernelEx(&cfg, esa::attn_q8_kernel<T, D, FMT, NT>, a));
-  ESA_LAUNCH_CHECK("attn_q8_kernel");
-  return ok();
+  const esa_status_t ls = launch_q8(esa::attn_q8_kernel<T, D, FMT, NT>, "attn_q8_kernel", grid, esa::kQ8Threads, smem,
+                                    csize, s, a);
+  return ls == ESA_OK ? ok() : ls;
 }
 template <typename T, int D>
 esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int nt, dim3 grid, int csize, cudaStream_t s) {
@@ -1354,21 +1369,10 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
   int csize = 1;
   for (int c = 2; c <= esa::kQtMaxCluster && c <= tiles; ++c)
     if (units <= ((fit >> (8 * (c - 2))) & 255)) csize = c;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(csize, a.hkv * a.tiles, batch);
-  cfg.blockDim = dim3(Sh::kThreads);
-  cfg.dynamicSmemBytes = Sh::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = csize;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  ESA_CUDA(cudaLaunchKernelEx(&cfg, esa::attn_q8_tc_kernel<FMT, WR, NWG>, a));
-  ESA_LAUNCH_CHECK("attn_q8_tc_kernel");
-  return ok();
+  const esa_status_t ls =
+      launch_q8(esa::attn_q8_tc_kernel<FMT, WR, NWG>, "attn_q8_tc_kernel", dim3(csize, a.hkv * a.tiles, batch),
+                Sh::kThreads, Sh::kSmem, csize, s, a);
+  return ls == ESA_OK ? ok() : ls;
 }
 // Rows in as few equal tiles as 24 rows allow, and the warpgroups that hold such a tile.
 template <int FMT>
@@ -1416,9 +1420,10 @@ esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, i
   a.bshift = log2_of(c.block);
   const esa::ReadTile tile(c.hkv * 8);
   const dim3 sgrid((unsigned)(cdiv(t_pad, tile.rows * esa::kReadPer) * tile.col_ctas), c.batch, 2);
-  if (c.format == ESA_Q8_E4M3) esa::cache_stage_q8_kernel<esa::kQ8E4M3><<<sgrid, esa::kReadThreads, 0, s>>>(a);
-  else esa::cache_stage_q8_kernel<esa::kQ8Int8><<<sgrid, esa::kReadThreads, 0, s>>>(a);
-  ESA_LAUNCH_CHECK("cache_stage_q8_kernel");
+  st = launch_q8(c.format == ESA_Q8_E4M3 ? esa::cache_stage_q8_kernel<esa::kQ8E4M3>
+                                         : esa::cache_stage_q8_kernel<esa::kQ8Int8>,
+                 "cache_stage_q8_kernel", sgrid, esa::kReadThreads, 0, 1, s, a);
+  if (st != ESA_OK) return st;
   esa::Q8TcProblem pr{};
   pr.q = static_cast<const __nv_bfloat16*>(q);
   pr.o = static_cast<__nv_bfloat16*>(o);
@@ -1559,15 +1564,13 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
   if (ctas >= ((int64_t)1 << 31)) return fail(ESA_ERR_UNSUPPORTED, "too many rows in one read");
   const dim3 grid((unsigned)ctas, cache.batch, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cache.format == ESA_Q8_E4M3) {
-    if (dt == ESA_BF16) esa::cache_read_q8_kernel<__nv_bfloat16, esa::kQ8E4M3><<<grid, esa::kReadThreads, 0, s>>>(a);
-    else esa::cache_read_q8_kernel<float, esa::kQ8E4M3><<<grid, esa::kReadThreads, 0, s>>>(a);
-  } else {
-    if (dt == ESA_BF16) esa::cache_read_q8_kernel<__nv_bfloat16, esa::kQ8Int8><<<grid, esa::kReadThreads, 0, s>>>(a);
-    else esa::cache_read_q8_kernel<float, esa::kQ8Int8><<<grid, esa::kReadThreads, 0, s>>>(a);
-  }
-  ESA_LAUNCH_CHECK("cache_read_q8_kernel");
-  return ok();
+  auto* kernel = cache.format == ESA_Q8_E4M3
+                     ? (dt == ESA_BF16 ? esa::cache_read_q8_kernel<__nv_bfloat16, esa::kQ8E4M3>
+                                       : esa::cache_read_q8_kernel<float, esa::kQ8E4M3>)
+                     : (dt == ESA_BF16 ? esa::cache_read_q8_kernel<__nv_bfloat16, esa::kQ8Int8>
+                                       : esa::cache_read_q8_kernel<float, esa::kQ8Int8>);
+  const esa_status_t ls = launch_q8(kernel, "cache_read_q8_kernel", grid, esa::kReadThreads, 0, 1, s, a);
+  return ls == ESA_OK ? ok() : ls;
 }
 
 size_t esa_sparse_attn_q8_workspace_size(int32_t batch, int32_t lq, int64_t c0, int32_t hq, int32_t hkv,
