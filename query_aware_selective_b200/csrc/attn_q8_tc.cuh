@@ -19,10 +19,10 @@
 // tile's largest at worst; three int8 digits, 2^-21, showed in dims where the largest
 // weight's value is next to zero), and nothing in TMEM is ever rescaled.
 //
-// Roles: one to three softmax warpgroups of up to 8 query rows each (thread = key for S and
-// W, thread = dim for O), one warp that issues the MMAs, two that copy keys, values and
-// scales (16-byte cp.async, 8 lanes a row, into 128-byte-swizzled tiles). TMEM: S and O, two
-// buffers each. A CTA takes a share of one (sequence, KV head)'s key list; at the end each
+// Roles: one to three softmax warpgroups (thread = key for S and W, thread = dim for O; up to
+// 8 query rows each, and with few rows two that take turns at the key tiles), one warp that issues the MMAs, two that copy keys, values and
+// scales (16-byte cp.async, 8 lanes a row, into 128-byte-swizzled tiles). TMEM: four
+// buffers of S (two where N leaves no room), two of O. A CTA takes a share of one (sequence, KV head)'s key list; at the end each
 // CTA of a cluster sends every other its part of their dims and merges its own.
 #pragma once
 #include "attn_q8.cuh"
@@ -36,49 +36,58 @@ constexpr uint32_t kQtTile = 128 * 128;                       // bytes of a key 
 constexpr uint32_t kQtStage = 2 * kQtTile + 2 * kQtKeys * 4;  // keys, values, their scales
 constexpr int kQtMaxCluster = 8;
 
-// WR query rows per softmax warpgroup, NWG warpgroups: RT rows of a tile.
-template <int FMT, int WR, int NWG>
+// RG row groups of WR query rows (RT rows of a tile) times TG tile groups: the warpgroup of
+// row group rg and tile group tg takes those rows of the key tiles j with j % TG == tg.
+template <int FMT, int WR, int RG, int TG>
 struct QtShape {
-  static constexpr int RT = WR * NWG;
+  static constexpr int RT = WR * RG;
   static constexpr int NQ = FMT == kQ8E4M3 ? 2 : 3, NW = FMT == kQ8E4M3 ? 3 : 4;   // pieces of a query, of a weight
   static constexpr int N = (NW * RT + 15) / 16 * 16;          // MMA columns (M = 128: a multiple of 16)
-  static constexpr int kThreads = (4 * NWG + 3) * 32;
-  static constexpr int kCtas = RT <= 4 ? 2 : 1;               // per SM
-  static constexpr int kStages = kCtas == 2 ? 3 : 5;
-  static constexpr uint32_t kCols = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;   // TMEM columns
+  static constexpr int kThreads = (4 * RG * TG + 3) * 32;
+  static constexpr int kStages = RT <= 8 ? 6 : 5;
+  static constexpr int NS = 6 * N <= 512 ? 4 : 2;             // score buffers in TMEM (O: two behind them)
+  static constexpr uint32_t kCols = (NS + 2) * N <= 128 ? 128 : (NS + 2) * N <= 256 ? 256 : 512;   // TMEM columns
   static constexpr uint32_t kQ = kStages * kQtStage, kW = kQ + N * 128, kCtrl = kW + 2 * N * 128;
-  // behind the control block, in floats: tile maxima [2][4][RT], l of each warp [4][RT] (at
-  // first the logit factors [RT]), and what the cluster's CTAs send: (m, l) [8][RT][2], o
-  // [RT][128] (128 / csize dims of each CTA)
-  static constexpr int kMax = 0, kL = 8 * RT, kMl = 12 * RT, kO = kMl + 2 * kQtMaxCluster * RT;
-  static constexpr int kOFloats = 160 * RT;                   // csize * q8_dims_per(csize) <= 160
-  static constexpr uint32_t kRing = kCtrl + 256 + (kO + kOFloats) * 4;   // list entries [stage][128]
+  // behind the control block, in floats: tile maxima [2][4][RT], logit factors [RT], l of
+  // each warp [TG][4][RT], and what the warpgroups of the cluster's CTAs send: (m, l)
+  // [8 TG][RT][2], o [RT][csize TG][dims of this CTA]
+  static constexpr int kMax = 0, kXs = 8 * RT, kL = 9 * RT, kMl = kL + 4 * TG * RT + (RT & 4 ? 4 : 0);
+  static constexpr int kO = kMl + 2 * kQtMaxCluster * TG * RT, kOFloats = 160 * TG * RT;   // csize * q8_dims_per <= 160
+  static constexpr uint32_t kRing = kCtrl + 256 + (kO + kOFloats) * 4;                     // list entries [stage][128]
   static constexpr uint32_t kSmem = kRing + kStages * 512;
-  static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024 && 4 * N * kCtas <= 512, "does not fit an SM");
+  static_assert(kSmem <= 232448 && (NS + 2) * N <= 512 && (kMl * 4) % 16 == 0 && (kO * 4) % 16 == 0, "does not fit an SM");
 };
 
 struct QtCtrl {
-  uint64_t full[5], empty[5], s_full[2], w_full[2], o_full[2], q_full, mma_done;
+  uint64_t full[6], empty[6], s_full[4], w_full[2], o_full[2], q_full, mma_done;
   uint32_t tmem_base;
   int abort_flag;
 };
 static_assert(sizeof(QtCtrl) <= 256, "control block overflows its reservation");
 
+// D[tmem] (+)= A[smem] * B[smem]^T on 8-bit codes, issued by one elected lane of a converged
+// warp (descriptors as low and high words: only the low one moves).
 template <int FMT>
-__device__ __forceinline__ void umma_q8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
+__device__ __forceinline__ void umma_q8_elect(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                              uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   if constexpr (FMT == kQ8E4M3) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
   }
 }
 // Instruction descriptor: e4m3 x e4m3 -> fp32, or s8 x s8 -> s32.
@@ -162,12 +171,12 @@ __device__ __forceinline__ void q8_split2(float x0, float x1, uint32_t* pc) {
 __device__ __forceinline__ int q8_dims_per(int csize) { return ((128 + csize - 1) / csize + 3) & ~3; }
 
 // grid (cluster size, Hkv * tiles, B), cluster (cluster size, 1, 1); a.hc = 1.
-template <int FMT, int WR, int NWG>
-__global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FMT, WR, NWG>::kCtas))
-    attn_q8_tc_kernel(const AttnQ8Args a) {
-  using Sh = QtShape<FMT, WR, NWG>;
-  constexpr int RT = Sh::RT, N = Sh::N, NST = Sh::kStages, NQ = Sh::NQ, NW = Sh::NW;
-  constexpr int kMmaWarp = 4 * NWG, kProdWarp = kMmaWarp + 1, kSoftThreads = 128 * NWG;
+template <int FMT, int WR, int RG, int TG>
+__global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_q8_tc_kernel(const AttnQ8Args a) {
+  using Sh = QtShape<FMT, WR, RG, TG>;
+  constexpr int RT = Sh::RT, N = Sh::N, NST = Sh::kStages, NS = Sh::NS, NQ = Sh::NQ, NW = Sh::NW;
+  constexpr int kMmaWarp = 4 * RG * TG, kProdWarp = kMmaWarp + 1, kSoftThreads = 128 * RG * TG;
+  constexpr int kBarTmem = RG * TG + 1, kBarQ = RG * TG + 2;      // named barriers (1 .. RG * TG: the warpgroups)
   // a weight of 1 (its tile's largest) goes in as 2^8 (e4m3, <= 448), 2^27 (int8, <= 127 * 2^21)
   constexpr float kTop = FMT == kQ8E4M3 ? 8.f : 27.f;
   // units of the first piece of a query and of a weight
@@ -178,6 +187,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
   QtCtrl& sm = *reinterpret_cast<QtCtrl*>(qtsm + Sh::kCtrl);
   float* const smf = reinterpret_cast<float*>(qtsm + Sh::kCtrl + 256);
   float* const sm_l = smf + Sh::kL;
+  float* const sm_xs = smf + Sh::kXs;
 
   const int g = blockIdx.y / a.tiles, tile = blockIdx.y - g * a.tiles, b = blockIdx.z;
   const int rank = blockIdx.x, csize = gridDim.x;
@@ -209,12 +219,12 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
       mbar_init(&sm.full[s], 64);                   // every producer thread, when its copies have landed
       mbar_init(&sm.empty[s], 1);
     }
+    for (int s = 0; s < NS; ++s) mbar_init(&sm.s_full[s], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.w_full[s], 4 * NWG);
+      mbar_init(&sm.w_full[s], 4 * RG);
       mbar_init(&sm.o_full[s], 1);
     }
-    mbar_init(&sm.q_full, 4 * NWG);
+    mbar_init(&sm.q_full, 4 * RG);
     mbar_init(&sm.mma_done, 1);
     sm.abort_flag = base & 1023u ? 1 : 0;
     if (base & 1023u) record_status(5u, 710);
@@ -238,7 +248,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
       tmem_relinquish();
     }
     tc_fence_before();
-    asm volatile("bar.sync %0, %1;" ::"n"(NWG + 1), "n"(kSoftThreads + 32) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"n"(kBarTmem), "n"(kSoftThreads + 32) : "memory");
     tc_fence_after();
     tmem = sm.tmem_base;
   }
@@ -307,62 +317,74 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
     cp_async_wait_all();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = q8_idesc<FMT>(N, 0), idesc_o = q8_idesc<FMT>(N, 1);
-      const uint64_t dq = sdesc_sw128(base + Sh::kQ, 16, 1024);
-      bool ok = nt == 0 || mbar_wait(&sm.q_full, 0, abort_flag, 709);
-      // Whichever is ready next: S of tile js (its codes have landed, and js < jp + 2: the
-      // scores that were in its buffer have been read, as w_full[js - 2] says), or O of tile
-      // jp (its weights are written). Waiting for the two in a fixed order held O_j, and
-      // with it the release of a stage, until tile j + 1 had landed.
-      int js = 0, jp = 0;
-      uint64_t since = globaltimer_ns();
-      for (uint32_t spin = 0; ok && jp < nt;) {
-        if (jp < js && mbar_test_wait(&sm.w_full[jp & 1], (jp >> 1) & 1)) {
-          tc_fence_after();
-          const uint64_t dv = sdesc_sw128(base + (jp % NST) * kQtStage + kQtTile, 16, 1024);
-          const uint64_t dw = sdesc_sw128(base + Sh::kW + (jp & 1) * N * 128, 16, 1024);
+    // The warp runs converged and one elected lane issues (by lane 0 alone, in a branch, the
+    // four MMAs and two commits of a product took 800 cycles: the pace of the whole kernel).
+    constexpr uint32_t idesc_s = q8_idesc<FMT>(N, 0), idesc_o = q8_idesc<FMT>(N, 1);
+    const uint64_t dsc = sdesc_sw128(base, 16, 1024);
+    const uint32_t d_lo = (uint32_t)dsc, d_hi = (uint32_t)(dsc >> 32);     // of the start of shared memory
+    bool ok = nt == 0 || mbar_wait_warp(&sm.q_full, 0, abort_flag, 709);
+    // Whichever is ready next: O of tile jp (its weights are written), or S of tile js (its
+    // codes have landed, and js < jp + NS: the scores that were in its buffer have been read,
+    // as the weights of tile js - NS say). Waiting for the two in a fixed order held O_j, and
+    // with it the release of a stage, until tile j + 1 had landed; with NS of 2 a warpgroup
+    // waited for its own O before it got new scores.
+    int js = 0, jp = 0, ss = 0, sp = 0;                                    // tiles and their stages
+    uint32_t fs = 0;                                                       // phase of full[ss]
+    uint64_t since = globaltimer_ns();
+    for (uint32_t spin = 0; ok && jp < nt;) {
+      if (jp < js && __all_sync(0xffffffffu, mbar_test_wait(&sm.w_full[jp & 1], (jp >> 1) & 1))) {
+        tc_fence_after();
+        const uint32_t v_lo = d_lo + ((sp * kQtStage + kQtTile) >> 4), w_lo = d_lo + ((Sh::kW + (jp & 1) * N * 128) >> 4);
+        const uint32_t d = tmem + (NS + (jp & 1)) * N;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)            // 32 keys: four 8-row groups of V, 32 bytes of a W row
-            umma_q8<FMT>(tmem + (2 + (jp & 1)) * N, dv + kk * 256, dw + kk * 2, idesc_o, kk > 0);
-          umma_commit(&sm.o_full[jp & 1]);
-          umma_commit(&sm.empty[jp % NST]);
-          ++jp;
-          spin = 0;
-        } else if (js < nt && js < jp + 2 && mbar_test_wait(&sm.full[js % NST], (js / NST) & 1)) {
-          fence_proxy_async();                      // cp.async wrote through the generic proxy
-          tc_fence_after();
-          const uint64_t dk = sdesc_sw128(base + (js % NST) * kQtStage, 16, 1024);
+        for (int kk = 0; kk < 4; ++kk)              // 32 keys: four 8-row groups of V, 32 bytes of a W row
+          umma_q8_elect<FMT>(d, v_lo + kk * 256, d_hi, w_lo + kk * 2, d_hi, idesc_o, kk > 0);
+        umma_commit_elect(&sm.o_full[jp & 1]);
+        umma_commit_elect(&sm.empty[sp]);
+        ++jp;
+        sp = sp + 1 == NST ? 0 : sp + 1;
+        spin = 0;
+      } else if (js < nt && js < jp + NS && __all_sync(0xffffffffu, mbar_test_wait(&sm.full[ss], fs))) {
+        fence_proxy_async();                        // cp.async wrote through the generic proxy
+        tc_fence_after();
+        const uint32_t k_lo = d_lo + ((ss * kQtStage) >> 4), q_lo = d_lo + (Sh::kQ >> 4);
+        const uint32_t d = tmem + (js % NS) * N;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_q8<FMT>(tmem + (js & 1) * N, dk + kk * 2, dq + kk * 2, idesc_s, kk > 0);
-          umma_commit(&sm.s_full[js & 1]);
-          ++js;
-          spin = 0;
-        } else if (spin++ == 0) {
-          since = globaltimer_ns();
-        } else if ((spin & 255u) == 0) {
-          if (*abort_flag) ok = false;
-          else if (globaltimer_ns() - since > ESA_WAIT_LIMIT_NS) {
-            *abort_flag = 1;
-            record_status(4u, 708);
-            ok = false;
-          }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_q8_elect<FMT>(d, k_lo + kk * 2, d_hi, q_lo + kk * 2, d_hi, idesc_s, kk > 0);
+        umma_commit_elect(&sm.s_full[js % NS]);
+        ++js;
+        if (++ss == NST) {
+          ss = 0;
+          fs ^= 1;
         }
+        spin = 0;
+      } else if (spin++ == 0) {
+        since = globaltimer_ns();
+      } else if ((spin & 255u) == 0) {
+        bool stop = *abort_flag;
+        if (!stop && globaltimer_ns() - since > ESA_WAIT_LIMIT_NS) {
+          *abort_flag = 1;
+          if (lane == 0) record_status(4u, 708);
+          stop = true;
+        }
+        ok = !__any_sync(0xffffffffu, stop);
       }
-      // every MMA issued so far has completed before TMEM and shared memory are reused
-      umma_commit(&sm.mma_done);
-      mbar_wait(&sm.mma_done, 0, abort_flag, 714, /*respect_abort=*/false);
     }
+    // every MMA issued so far has completed before TMEM and shared memory are reused
+    umma_commit_elect(&sm.mma_done);
+    mbar_wait(&sm.mma_done, 0, abort_flag, 714, /*respect_abort=*/false);
     __syncwarp();
   } else {
     // ------------------------------------------------------------------- softmax warps
-    const int wg = NWG == 1 ? 0 : warp >> 2, key = threadIdx.x & 127;    // key of a tile, for S and W; the dim, for O
-    const uint32_t bar_wg = 1 + wg;                       // named barrier of the warpgroup
-    const int row_wg = wg * WR;                           // its first row of the tile
+    const int rg = (warp >> 2) % RG, tg = (warp >> 2) / RG;
+    const int key = threadIdx.x & 127;                    // key of a tile, for S and W; the dim, for O
+    const uint32_t bar_wg = 1 + (warp >> 2);              // named barrier of the warpgroup
+    const int row_wg = rg * WR;                           // its first row of the tile
     // queries as pieces: thread (r, part) takes DPT dims of row r
     constexpr int TPR = 128 / WR, DPT = 128 / TPR;
     float xs[WR];                                   // logit factor of each row
-    {
+    if (tg == 0) {
       const int r = row_wg + key / TPR, part = key % TPR;
       const int rr = min(r0 + r, a.lq * a.G - 1), i = rr / a.G, hl = rr - i * a.G;
       const __nv_bfloat16* qp =
@@ -380,7 +402,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
       // 2^qe brings the row's largest to [2^7, 2^8) (e4m3) or [2^19, 2^20) (int8)
       const int qe = min((FMT == kQ8E4M3 ? 7 : 19) - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127), 100);
       const float up = __uint_as_float((uint32_t)(qe + 127) << 23);
-      if (part == 0) sm_l[r] = a.scale_log2 * kUnitQ * __uint_as_float((uint32_t)(127 - qe) << 23);
+      if (part == 0) sm_xs[r] = a.scale_log2 * kUnitQ * __uint_as_float((uint32_t)(127 - qe) << 23);
       const uint32_t q0 = base + Sh::kQ;
 #pragma unroll
       for (int e = 0; e < DPT; e += 4) {
@@ -399,31 +421,33 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
       // columns that belong to no piece: zero in the queries and in both weight buffers
       if constexpr (N > NW * RT) {
         constexpr int pad = (N - NW * RT) * 8;          // 16-byte pieces of a buffer (W follows Q)
-        for (int z = threadIdx.x; z < 3 * pad; z += kSoftThreads)
+        for (int z = threadIdx.x; z < 3 * pad; z += 128 * RG)
           st_shared_v4(base + Sh::kQ + ((z / pad) * N + NW * RT) * 128 + (z % pad) * 16, 0u, 0u, 0u, 0u);
       }
       fence_proxy_async();
       mbar_arrive_warp(&sm.q_full);
-      asm volatile("bar.sync %0, 128;" ::"r"(bar_wg) : "memory");
-#pragma unroll
-      for (int q = 0; q < WR; ++q) xs[q] = sm_l[row_wg + q];
     }
+    asm volatile("bar.sync %0, %1;" ::"n"(kBarQ), "n"(kSoftThreads) : "memory");
+#pragma unroll
+    for (int q = 0; q < WR; ++q) xs[q] = sm_xs[row_wg + q];
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + row_wg;
     float al[WR], be[WR];                           // the tile's factors on o and on its own O
+    auto spin_warp = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, site));
+    };
     auto drain = [&](int j) -> bool {               // o = o al + O_j be
-      if (!mbar_wait_warp(&sm.o_full[j & 1], (j >> 1) & 1, abort_flag, 712)) return false;
+      if (!spin_warp(&sm.o_full[j & 1], (j >> 1) & 1, 712)) return false;
       tc_fence_after();
       uint32_t v[NW * WR];
-      tmem_ld_pieces<NW, WR, RT>(lane_base + (2 + (j & 1)) * N, v);
+      tmem_ld_pieces<NW, WR, RT>(lane_base + (NS + (j & 1)) * N, v);
 #pragma unroll
       for (int r = 0; r < WR; ++r) o[r] = fmaf(o[r], al[r], q8_join<FMT, WR, NW>(v, r) * be[r]);
       return true;
     };
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
+    for (int j = tg; j < nt; j += TG) {
       // (full: the scales, which this warp reads itself)
-      ok = ok && mbar_wait_warp(&sm.s_full[j & 1], (j >> 1) & 1, abort_flag, 713) &&
-           mbar_wait_warp(&sm.full[j % NST], (j / NST) & 1, abort_flag, 715);
+      ok = ok && spin_warp(&sm.s_full[j % NS], (j / NS) & 1, 713) && spin_warp(&sm.full[j % NST], (j / NST) & 1, 715);
       tc_fence_after();
       float x[WR];
       const float* sc = reinterpret_cast<const float*>(qtsm + (j % NST) * kQtStage + 2 * kQtTile);
@@ -431,7 +455,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
       const float lv = __log2f(fmaxf(sc[kQtKeys + key], 0x1p-120f));
       {
         uint32_t v[NQ * WR];
-        tmem_ld_pieces<NQ, WR, RT>(lane_base + (j & 1) * N, v);
+        tmem_ld_pieces<NQ, WR, RT>(lane_base + (j % NS) * N, v);
 #pragma unroll
         for (int r = 0; r < WR; ++r) x[r] = fmaf(q8_join<FMT, WR, NQ>(v, r), ka * xs[r], lv);
       }
@@ -449,6 +473,9 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
         mt[r] = redux_max(x[r]);
         if (lane == 0) mx[(warp & 3) * RT + r] = mt[r];
       }
+      // the O of this warpgroup's tile before (PV_j will overwrite it if TG is 2, and the W
+      // buffer below was its own)
+      if (j >= TG) ok = ok && drain(j - TG);
       // a named barrier has no time limit: the four warps leave together if a wait ran out
       if (!(ok = bar_all(bar_wg, 128, ok))) break;
 #pragma unroll
@@ -473,7 +500,6 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive_warp(&sm.w_full[j & 1]);
-      if (j > 0) ok = drain(j - 1);                 // (a wait that ran out: the next bar_all)
 #pragma unroll
       for (int r = 0; r < WR; ++r) {
         const float mn = fmaxf(m[r], mt[r]);
@@ -485,27 +511,29 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
         m[r] = mn;
       }
     }
-    if (nt > 0 && ok) ok = drain(nt - 1);
+    const int last = (nt - 1 - tg) / TG * TG + tg;  // the warpgroup's last tile, if it had one
+    if (tg < nt && ok) ok = drain(last);
 
     // ---- the CTA's row sums, then every CTA of the cluster gets its share of the dims (dim
     // d belongs to CTA d / per) and all (m, l)
-    asm volatile("bar.sync %0, 128;" ::"r"(bar_wg) : "memory");      // (xs have been read)
 #pragma unroll
     for (int r = 0; r < WR; ++r) {
       const float s = warp_sum(l[r]);
-      if (lane == 0) sm_l[(warp & 3) * RT + row_wg + r] = s;
+      if (lane == 0) sm_l[(tg * 4 + (warp & 3)) * RT + row_wg + r] = s;
     }
     if (csize > 1) cluster_wait();
     const int per = q8_dims_per(csize), owner = key / per, slot = key - owner * per;
     const uint32_t my_o = smem_u32(smf + Sh::kO), my_ml = smem_u32(smf + Sh::kMl);
-    const uint32_t dst = dsmem_map(my_o, owner) + (rank * per + slot) * 4;
+    const int part = rank * TG + tg, parts = csize * TG;
+    const uint32_t dst = dsmem_map(my_o, owner) + (part * per + slot) * 4;
 #pragma unroll
-    for (int r = 0; r < WR; ++r) st_dsmem_f32(dst + (row_wg + r) * per * csize * 4, o[r]);
+    for (int r = 0; r < WR; ++r) st_dsmem_f32(dst + (row_wg + r) * per * parts * 4, o[r]);
     asm volatile("bar.sync %0, 128;" ::"r"(bar_wg) : "memory");
     for (int it = key; it < WR * csize; it += 128) {
       const int to = it / WR, r = row_wg + it % WR;
-      const float L = (sm_l[r] + sm_l[RT + r]) + (sm_l[2 * RT + r] + sm_l[3 * RT + r]);
-      const uint32_t p = dsmem_map(my_ml, to) + (rank * RT + r) * 8;
+      const float* lw = sm_l + tg * 4 * RT + r;
+      const float L = (lw[0] + lw[RT]) + (lw[2 * RT] + lw[3 * RT]);
+      const uint32_t p = dsmem_map(my_ml, to) + (part * RT + r) * 8;
       float mm = m[0];
 #pragma unroll
       for (int q = 1; q < WR; ++q) mm = it % WR == q ? m[q] : mm;
@@ -523,13 +551,14 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, NWG>::kThreads), (QtShape<FM
   const int per = q8_dims_per(csize), d0 = rank * per, d = lane * 4;
   if (d >= min(per, 128 - d0)) return;
   for (int r = warp; r < nrow; r += Sh::kThreads / 32) {         // a row per warp, four dims per lane
-    const float* ml = smf + Sh::kMl + r * 2;        // [csize][RT][2]
-    const float* po = smf + Sh::kO + r * per * csize + d;
+    const int parts = csize * TG;
+    const float* ml = smf + Sh::kMl + r * 2;        // [parts][RT][2]
+    const float* po = smf + Sh::kO + r * per * parts + d;
     float M = -INFINITY;
-    for (int u = 0; u < csize; ++u) M = fmaxf(M, ml[u * RT * 2]);
+    for (int u = 0; u < parts; ++u) M = fmaxf(M, ml[u * RT * 2]);
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int u = 0; u < csize; ++u) {
+    for (int u = 0; u < parts; ++u) {
       const float2 z = *reinterpret_cast<const float2*>(ml + u * RT * 2);
       const float4 x = *reinterpret_cast<const float4*>(po + u * per);
       const float c = fast_exp2(z.x - (M == -INFINITY ? 0.f : M));

@@ -1329,19 +1329,17 @@ esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int nt, dim3
                  : launch_attn_q8<T, D, esa::kQ8Int8, 2>(a, grid, csize, s);
 }
 
-template <int FMT, int WR, int NWG>
+template <int FMT, int WR, int RG, int TG>
 esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cudaStream_t s) {
-  using Sh = esa::QtShape<FMT, WR, NWG>;
+  using Sh = esa::QtShape<FMT, WR, RG, TG>;
   static const char what = 0;
   const esa_status_t st =
-      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_tc_kernel<FMT, WR, NWG>, Sh::kSmem); });
+      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_tc_kernel<FMT, WR, RG, TG>, Sh::kSmem); });
   if (st != ESA_OK) return st;
   a.tiles = (int)cdiv((int64_t)a.lq * a.G, Sh::RT);
   if ((int64_t)a.hkv * a.tiles > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
   // How many clusters of 2 .. 8 CTAs fit the GPU at once (a byte each; the SMs of a GPC do not
   // divide by every size: 24 clusters of 6 CTAs of one per SM left 8 CTAs to a second wave).
-  // The query counts one CTA of this kernel per SM; where shared memory, registers and TMEM
-  // are laid out for two, as many clusters again fit beside the first.
   static const char fits = 0;
   intptr_t fit = 0;
   const esa_status_t qs = per_context(&fits, &fit, [](intptr_t* v) {
@@ -1358,8 +1356,8 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
       q.attrs = at;
       q.numAttrs = 1;
       int n = 0;
-      ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, esa::attn_q8_tc_kernel<FMT, WR, NWG>, &q));
-      *v |= (intptr_t)std::min(n * Sh::kCtas, 255) << (8 * (c - 2));
+      ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, esa::attn_q8_tc_kernel<FMT, WR, RG, TG>, &q));
+      *v |= (intptr_t)std::min(n, 255) << (8 * (c - 2));
     }
     return ESA_OK;
   });
@@ -1370,7 +1368,7 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
   for (int c = 2; c <= esa::kQtMaxCluster && c <= tiles; ++c)
     if (units <= ((fit >> (8 * (c - 2))) & 255)) csize = c;
   const esa_status_t ls =
-      launch_q8(esa::attn_q8_tc_kernel<FMT, WR, NWG>, "attn_q8_tc_kernel", dim3(csize, a.hkv * a.tiles, batch),
+      launch_q8(esa::attn_q8_tc_kernel<FMT, WR, RG, TG>, "attn_q8_tc_kernel", dim3(csize, a.hkv * a.tiles, batch),
                 Sh::kThreads, Sh::kSmem, csize, s, a);
   return ls == ESA_OK ? ok() : ls;
 }
@@ -1378,10 +1376,10 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
 template <int FMT>
 esa_status_t dispatch_attn_q8_tc(const esa::AttnQ8Args& a, int32_t batch, int64_t n_keys, cudaStream_t s) {
   const int64_t rows = (int64_t)a.lq * a.G, rt = cdiv(rows, cdiv(rows, 24));
-  if (rt <= 4) return launch_attn_q8_tc<FMT, 4, 1>(a, batch, n_keys, s);
-  if (rt <= 8) return launch_attn_q8_tc<FMT, 8, 1>(a, batch, n_keys, s);
-  if (rt <= 16) return launch_attn_q8_tc<FMT, 8, 2>(a, batch, n_keys, s);
-  return launch_attn_q8_tc<FMT, 8, 3>(a, batch, n_keys, s);
+  if (rt <= 4) return launch_attn_q8_tc<FMT, 4, 1, 2>(a, batch, n_keys, s);
+  if (rt <= 8) return launch_attn_q8_tc<FMT, 8, 1, 2>(a, batch, n_keys, s);
+  if (rt <= 16) return launch_attn_q8_tc<FMT, 8, 2, 1>(a, batch, n_keys, s);
+  return launch_attn_q8_tc<FMT, 8, 3, 1>(a, batch, n_keys, s);
 }
 
 // The chunk form: the key list dequantised into the workspace, then attn_tc_kernel.
