@@ -460,11 +460,12 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  *   idx, count: [batch, lists, p.topk] and [batch, lists] int32, as the selections write them
  *   lse:        NULL or [batch, lq, hq] fp32
  * Scales may be any positive numbers below 2^121. hq is a multiple of hkv; no limit on
- * their ratio. Codes are exact in the products; softmax weights are rounded to f16 (bf16
- * for a chunk on the tensor-core path, see the workspace), and not at all for fp32 (22
- * bits). The workspace (esa_sparse_attn_q8_workspace_size bytes, 256-byte aligned) holds a
- * chunk's keys and values as bf16 (bf16, head_dim 128, hq / hkv in {1, 2, 4, 8} and
- * lq * hq / hkv >= 64); 0 bytes otherwise. Other errors as for esa_sparse_attn. */
+ * their ratio. Codes are exact in the products; softmax weights keep 11 bits or more (22
+ * for fp32), and 2^-26 of the largest at least. A large chunk (bf16, head_dim 128, hq / hkv in {1, 2, 4, 8}) dequantises its
+ * keys and values into the workspace as bf16 (exact for scales that are powers of two) and
+ * rounds its weights to bf16. The workspace is for that alone: ask
+ * esa_sparse_attn_q8_workspace_size (256-byte aligned; 0 bytes for other calls). Other
+ * errors as for esa_sparse_attn. */
 esa_status_t esa_sparse_attn_q8(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, int32_t lq, int64_t c0,
                                 int32_t hq, const int32_t* idx, const int32_t* count, int32_t lists,
                                 esa_params_t p, float scale, void* o, float* lse, void* workspace,

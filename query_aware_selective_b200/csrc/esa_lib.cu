@@ -1276,9 +1276,21 @@ esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int6
   return ls == ESA_OK ? ok() : ls;
 }
 
-bool q8_tensor_cores(int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
+// Query rows of a KV head in tiles of up to 24 (attn_q8_tc_kernel).
+int64_t q8_row_tiles(int64_t rows) { return cdiv(rows, 24); }
+
+// Whether a call dequantises its key list for attn_tc_kernel (128 rows a CTA, every CTA the
+// whole list: 62 to 65 us for 6.3K keys whatever the rows, until its CTAs outnumber the SMs)
+// or runs attn_q8_tc_kernel on the codes. The latter splits each list over clusters while
+// its units of work (sequence, KV head, 24 rows) leave SMs free for that: 22 us for 6.3K
+// keys with 24 units, 44 with up to 74, 80 with up to 148, a wave more for each further
+// 148. So: codes up to half the SMs' number of units (and under 64 rows, whose 128-row
+// tiles would be half empty), the tensor-core chunk above.
+bool q8_chunk_form(int64_t batch, int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
   const int g = hq / hkv;
-  return dt == ESA_BF16 && head_dim == 128 && (int64_t)lq * g >= 64 && (g == 1 || g == 2 || g == 4 || g == 8);
+  const int64_t rows = (int64_t)lq * g;
+  return dt == ESA_BF16 && head_dim == 128 && rows >= 64 && (g == 1 || g == 2 || g == 4 || g == 8) &&
+         batch * hkv * q8_row_tiles(rows) > 74;
 }
 
 int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
@@ -1375,7 +1387,7 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
 // Rows in as few equal tiles as 24 rows allow, and the warpgroups that hold such a tile.
 template <int FMT>
 esa_status_t dispatch_attn_q8_tc(const esa::AttnQ8Args& a, int32_t batch, int64_t n_keys, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.lq * a.G, rt = cdiv(rows, cdiv(rows, 24));
+  const int64_t rows = (int64_t)a.lq * a.G, rt = cdiv(rows, q8_row_tiles(rows));
   if (rt <= 4) return launch_attn_q8_tc<FMT, 4, 1, 2>(a, batch, n_keys, s);
   if (rt <= 8) return launch_attn_q8_tc<FMT, 8, 1, 2>(a, batch, n_keys, s);
   if (rt <= 16) return launch_attn_q8_tc<FMT, 8, 2, 1>(a, batch, n_keys, s);
@@ -1468,7 +1480,7 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   esa::KeyList keys{idx, p.topk, r.ni, r.lo, c.n_cap, count};
   if (seq_len) keys.vl = esa::VarLen{seq_len, c.n_cap, p.n_init, p.window, 1};
-  else if (q8_tensor_cores(lq, hq, c.hkv, c.head_dim, dt)) {
+  else if (q8_chunk_form(c.batch, lq, hq, c.hkv, c.head_dim, dt)) {
     const size_t need = esa_sparse_attn_q8_workspace_size(c.batch, lq, c0, hq, c.hkv, c.head_dim, dt, p);
     if (!workspace || ws_bytes < need || !aligned(workspace, 256))
       return fail(ESA_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
@@ -1476,10 +1488,7 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
   }
   const int g = hq / c.hkv;
   const int64_t rows = (int64_t)lq * g;
-  const int nt = rows <= 8 ? 1 : 2;
-  const int64_t tiles = cdiv(rows, 8 * nt);
-  const Q8Plan pl = plan_q8(c.batch, tiles, c.hkv, r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq);
-  if (tiles * (c.hkv / pl.hc) > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
+  const int64_t n_keys = r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq;
   esa::AttnQ8Args a{};
   a.q = q;
   a.k = static_cast<const uint8_t*>(c.k);
@@ -1498,18 +1507,19 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
   a.G = g;
   a.lists = lists;
   a.bshift = log2_of(c.block);
-  a.hc = pl.hc;
-  a.tiles = (int)tiles;
   a.scale_log2 = sl2;
-  if (dt == ESA_BF16 && c.head_dim == 128) {
-    const int64_t n_keys = r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq;
+  if (dt == ESA_BF16 && c.head_dim == 128)
     return c.format == ESA_Q8_E4M3 ? dispatch_attn_q8_tc<esa::kQ8E4M3>(a, c.batch, n_keys, s)
                                    : dispatch_attn_q8_tc<esa::kQ8Int8>(a, c.batch, n_keys, s);
-  }
+  // fp32 queries (22 bits of them and of the weights) and heads of 64
+  const int nt = rows <= 8 ? 1 : 2;
+  const int64_t tiles = cdiv(rows, 8 * nt);
+  const Q8Plan pl = plan_q8(c.batch, tiles, c.hkv, n_keys);
+  if (tiles * (c.hkv / pl.hc) > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
+  a.hc = pl.hc;
+  a.tiles = (int)tiles;
   const dim3 grid((unsigned)pl.csize, (unsigned)(tiles * (c.hkv / pl.hc)), c.batch);
-  if (dt == ESA_BF16)
-    return c.head_dim == 128 ? dispatch_attn_q8<__nv_bfloat16, 128>(a, c.format, nt, grid, pl.csize, s)
-                             : dispatch_attn_q8<__nv_bfloat16, 64>(a, c.format, nt, grid, pl.csize, s);
+  if (dt == ESA_BF16) return dispatch_attn_q8<__nv_bfloat16, 64>(a, c.format, nt, grid, pl.csize, s);
   return c.head_dim == 128 ? dispatch_attn_q8<float, 128>(a, c.format, nt, grid, pl.csize, s)
                            : dispatch_attn_q8<float, 64>(a, c.format, nt, grid, pl.csize, s);
 }
@@ -1574,7 +1584,7 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
 size_t esa_sparse_attn_q8_workspace_size(int32_t batch, int32_t lq, int64_t c0, int32_t hq, int32_t hkv,
                                          int32_t head_dim, esa_dtype_t dt, esa_params_t p) {
   if (batch <= 0 || lq <= 0 || c0 < 0 || hkv <= 0 || hq <= 0 || hq % hkv) return 0;
-  if (!q8_tensor_cores(lq, hq, hkv, head_dim, dt)) return 0;
+  if (!q8_chunk_form(batch, lq, hq, hkv, head_dim, dt)) return 0;
   return 2 * up256((size_t)batch * q8_staged_rows(lq, c0, p) * hkv * head_dim * 2);
 }
 
