@@ -120,11 +120,18 @@ class _Compressor:
 class EsaPrefill:
     """Chunked prefill of one attention layer: for every chunk [c0, c0 + chunk),
     compress the chunk's keys into the compressed cache, compress its queries,
-    select middle tokens, attend over initial + selected + local."""
+    select middle tokens, attend over initial + selected + local. With cache (a CacheQ8 of
+    the same batch and heads, n_cap >= n_ctx) every chunk's keys and values are quantised
+    into it before its attention, which runs over the cache: what a decode over that cache
+    will see."""
 
     def __init__(self, batch: int, n_ctx: int, chunk: int, hq: int, hkv: int, head_dim: int, d_c: int,
                  p: _abi.EsaParams, dtype=torch.bfloat16, device="cuda", per_head: bool = False,
-                 key_chunks: int = 2):
+                 key_chunks: int = 2, cache: Optional[_abi.CacheQ8] = None):
+        if cache is not None and (cache.k.shape[0] != batch or cache.k.shape[1] < n_ctx or
+                                  cache.k.shape[2:] != (hkv, head_dim)):
+            raise ValueError("the cache must be [batch, >= n_ctx, hkv, head_dim]")
+        self.cache = cache
         self.batch, self.n_ctx, self.chunk = batch, n_ctx, chunk
         self.key_chunks = key_chunks      # chunks whose keys run() compresses in one launch
         self.hq, self.hkv, self.d, self.d_c, self.p = hq, hkv, head_dim, d_c, p
@@ -151,6 +158,10 @@ class EsaPrefill:
                          for c0 in range(0, n_ctx, chunk))
             ws_att = max(_abi.sparse_attn_workspace_size(batch, min(chunk, n_ctx - c0), c0, hq, hkv, head_dim, code,
                                                          p)
+                         for c0 in range(0, n_ctx, chunk))
+        if cache is not None:
+            ws_att = max(_abi.sparse_attn_q8_workspace_size(batch, min(chunk, n_ctx - c0), c0, hq, hkv, head_dim,
+                                                            code, p)
                          for c0 in range(0, n_ctx, chunk))
         self.ws_sel = torch.empty(ws_sel + 256, dtype=torch.uint8, device=device)
         self.ws_att = torch.empty(ws_att + 256, dtype=torch.uint8, device=device) if ws_att else None
@@ -192,10 +203,16 @@ class EsaPrefill:
             qv = qv.contiguous()
         ov = self.out[:, c0:c0 + lq]
         target = ov if ov.is_contiguous() else torch.empty_like(ov)
+        if self.cache is not None:
+            _abi.cache_write_q8(self.cache, k[:, c0:c0 + lq], v[:, c0:c0 + lq], c0)
         if attn_events is not None:
             attn_events[0].record()
-        attn = _abi.sparse_attn_heads if self.per_head else _abi.sparse_attn
-        attn(qv, k, v, c0, self.idx_all[ci], self.count_all[ci], self.p, out=target, workspace=self.ws_att)
+        if self.cache is not None:
+            _abi.sparse_attn_q8(qv, self.cache, c0, self.idx_all[ci], self.count_all[ci], self.p, out=target,
+                                workspace=self.ws_att)
+        else:
+            attn = _abi.sparse_attn_heads if self.per_head else _abi.sparse_attn
+            attn(qv, k, v, c0, self.idx_all[ci], self.count_all[ci], self.p, out=target, workspace=self.ws_att)
         if attn_events is not None:
             attn_events[1].record()
         if target is not ov:
@@ -449,6 +466,49 @@ class EsaDecodeVarlen:
         _abi.sparse_attn_varlen(q, k, v, seq_len, self.idx, self.count, self.p, out=self.out,
                                 workspace=self.ws_att)
         cur.wait_stream(self.side)
+        return self.out
+
+
+class EsaDecodeQ8(EsaDecodeVarlen):
+    """EsaDecodeVarlen over an 8-bit cache (a CacheQ8), which is the only place the keys and
+    values live: a step quantises the new token into it and attends over it, the selection
+    runs on the compressed keys as before."""
+
+    def __init__(self, cache: _abi.CacheQ8, hq: int, d_c: int, p: _abi.EsaParams, dtype=torch.bfloat16,
+                 per_head: bool = False):
+        batch, n_cap, hkv, head_dim = cache.k.shape
+        super().__init__(batch, n_cap, hq, hkv, head_dim, d_c, p, dtype=dtype, device=cache.device,
+                         per_head=per_head)
+        self.cache = cache
+        self.ws_att = None
+
+    def fill_cache(self, wk, lengths):
+        """Compress the cached keys [0, lengths[b] - 1) of every sequence (prefill state) as
+        the cache holds them; lengths: host integers."""
+        self.cmp.pack_keys(wk)
+        step = 1 << 12
+        for r0 in range(0, max(int(n) for n in lengths) - 1, step):
+            k, _ = _abi.cache_read_q8(self.cache, r0, min(step, self.n_cap - r0), want_v=False)
+            for s in range(self.batch):
+                r1 = min(int(lengths[s]) - 1, r0 + step)
+                if r1 > r0:
+                    self.cmp.keys(k[s, :r1 - r0], out=self.k_c[s, r0:r1])
+
+    def step(self, q, k_new, v_new, wq, wk, seq_len):
+        """q [B, 1, Hq, D]; k_new, v_new [B, Hkv, D] the new token's rows, which go to row
+        seq_len[b] - 1 of the cache; seq_len [B] int64 on the device, the new token counted."""
+        cur = torch.cuda.current_stream()
+        self.cmp.pack_if_changed(wq, wk)
+        # the new token is local to its own query: beside the selection, ahead of the attention
+        self.side.wait_stream(cur)
+        with torch.cuda.stream(self.side):
+            _abi.cache_write_q8_varlen(self.cache, k_new.unsqueeze(1), v_new.unsqueeze(1), seq_len)
+            _abi.compress_packed_varlen(k_new, self.cmp.wk_p, self.k_c, seq_len)
+        self.cmp.queries(q[:, 0], out=self.q_c.view(self.batch, self.d_c))
+        _abi.score_select_varlen(self.q_c, self.k_c, seq_len, self.p, n_groups=self.ng, idx=self.idx,
+                                 count=self.count, workspace=self.ws_sel)
+        cur.wait_stream(self.side)
+        _abi.sparse_attn_q8_varlen(q, self.cache, seq_len, self.idx, self.count, self.p, out=self.out)
         return self.out
 
 

@@ -23,6 +23,7 @@ import torch
 
 import query_aware_selective_b200 as qas
 from oracle import cache_q8 as oc
+from query_aware_selective_b200 import pipeline
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -678,3 +679,98 @@ def test_chunk_on_a_side_stream_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+# ------------------------------------------------------------------------ the pipelines --
+def _values(cache):
+    return tuple(np.nan_to_num(x.cpu().double().numpy()) for x in qas.cache_read_q8(cache, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("fmt,per_head", [("e4m3", False), ("int8", True)])
+def test_prefill_then_decode_over_one_cache(fmt, per_head):
+    """A prefill that fills the cache chunk by chunk, then decode steps that go on with it:
+    every output against the attention over the cache's own values and the selections made."""
+    b, n, chunk, hq, hkv, d, dc, block = 1, 1000, 256, 16, 4, 128, 128, 32
+    n_cap, n_init, window, topk = 1100, 64, 128, 200
+    p = qas.params(n_init, window, topk, 2, 45.25)
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn((b, n_cap, h, d), generator=g).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    if per_head:
+        wq, wk = (pipeline.block_diagonal(torch.randn((hkv, hq // hkv * d, dc // hkv), generator=g) / 32)
+                  for _ in range(2))
+    else:
+        wq, wk = (torch.randn((hq * d, dc), generator=g) / 32 for _ in range(2))
+    wq, wk = wq.to(DEV), wk.to(DEV)
+    cache = _cache(b, n_cap, hkv, d, fmt, block)
+    pf = pipeline.EsaPrefill(b, n, chunk, hq, hkv, d, dc, p, per_head=per_head, cache=cache)
+    plain = pipeline.EsaPrefill(b, n, chunk, hq, hkv, d, dc, p, per_head=per_head)
+    qd, kd, vd = (x[:, :n].contiguous().to(DEV) for x in (q, k, v))
+    out = pf.run(qd, kd, vd, wq, wk)
+    ref_out = plain.run(qd, kd, vd, wq, wk)
+    qas.device_status()
+    assert torch.equal(pf.idx_all, plain.idx_all)                  # the selection does not see the cache
+    # the chunks wrote what single writes of the same rows would have
+    want = _Oracle(b, n_cap, hkv, d, fmt, block)
+    for c0 in range(0, n, chunk):
+        want.write(0, k[0, c0:min(n, c0 + chunk)], v[0, c0:min(n, c0 + chunk)], c0)
+    want.check(cache)
+    kv, vv = _values(cache)
+    lists = hkv if per_head else 1
+    for ci, (c0, lq) in enumerate(pf.chunks()):
+        idx, cnt = pf.idx_all[ci].cpu().view(b, lists, topk), pf.count_all[ci].cpu().view(b, lists)
+        ws = qas._abi.sparse_attn_q8_workspace_size(b, lq, c0, hq, hkv, d, 1, p)
+        _check(out[:, c0:c0 + lq], None, _reference(q[:, c0:c0 + lq], kv, vv, [c0], idx, cnt, n_init, window),
+               torch.bfloat16, d, chunk=ws > 0)
+    # and stayed near the unquantised attention
+    err = float((out.float() - ref_out.float()).norm() / ref_out.float().norm())
+    assert err < (0.08 if fmt == "e4m3" else 0.03), err            # (2^-4 / 2^-7 a value at most, uncorrelated)
+
+    dec = pipeline.EsaDecodeQ8(cache, hq, dc, p, per_head=per_head)
+    dec.fill_cache(wk, [n + 1])
+    seq_len = torch.tensor([n], device=DEV)
+    for t in range(n, n + 5):
+        seq_len += 1
+        rows = [x[:, t].contiguous().to(DEV) for x in (k, v)]
+        o = dec.step(q[:, t:t + 1].contiguous().to(DEV), *rows, wq, wk, seq_len)
+        qas.device_status()
+        want.write(0, k[0, t:t + 1], v[0, t:t + 1], t)
+        want.check(cache)
+        kv, vv = _values(cache)
+        _check(o, None, _reference(q[:, t:t + 1], kv, vv, [t], dec.idx.cpu(), dec.count.cpu(), n_init, window),
+               torch.bfloat16, d)
+
+
+def test_decode_step_in_a_graph_with_lengths_that_differ():
+    b, n_cap, hq, hkv, d, dc = 3, 700, 8, 4, 128, 128
+    p = qas.params(32, 64, 100, 2, 45.25)
+    g = torch.Generator().manual_seed(6)
+    lens = [650, 90, 300]
+    wq, wk = ((torch.randn((hq * d, dc), generator=g) / 32).to(DEV) for _ in range(2))
+    k, v = (torch.randn((b, n_cap, hkv, d), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+
+    def make():
+        cache = _cache(b, n_cap, hkv, d, "int8", 64)
+        t = max(lens)
+        n = torch.tensor(lens, device=DEV)
+        qas.cache_write_q8_varlen(cache, k[:, :t], v[:, :t], n, n)
+        dec = pipeline.EsaDecodeQ8(cache, hq, dc, p)
+        dec.fill_cache(wk, [x + 1 for x in lens])
+        return dec, n
+    (a, na), (c, nc) = make(), make()
+    q = torch.randn((b, 1, hq, d), generator=g).to(torch.bfloat16).to(DEV)
+    kn, vn = (torch.randn((b, hkv, d), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    graph = pipeline.graph_of(lambda: a.step(q, kn, vn, wq, wk, na))       # (runs once: row len - 1 again)
+    c.step(q, kn, vn, wq, wk, nc)
+    for _ in range(4):
+        for x in (na, nc):
+            x += 1
+        kn.neg_()
+        q.mul_(1.25)
+        graph.replay()
+        c.step(q, kn, vn, wq, wk, nc)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, c.out)
+        assert torch.equal(a.cache.k.view(torch.uint8), c.cache.k.view(torch.uint8))
+        kv, vv = _values(c.cache)
+        _check(c.out, None, _reference(q.cpu(), kv, vv, [int(x) - 1 for x in nc], c.idx.cpu(), c.count.cpu(), 32, 64),
+               torch.bfloat16, d)
