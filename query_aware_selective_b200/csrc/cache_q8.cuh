@@ -19,6 +19,11 @@
 
 namespace esa {
 
+// Programmatic dependent launch: a kernel launched with the attribute may be set up while
+// the one before it in the stream still drains; nothing of global memory may be touched
+// before this wait, which returns once that kernel is complete and its writes are visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr int kQ8E4M3 = 0, kQ8Int8 = 1;
 constexpr int kQ8LeastExp = -100;          // scales stay normal, and so do their reciprocals
 

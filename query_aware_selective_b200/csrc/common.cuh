@@ -345,11 +345,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// Programmatic dependent launch: a kernel launched with the attribute may be set up while
-// the one before it in the stream still drains; nothing of global memory may be touched
-// before this wait, which returns once that kernel is complete and its writes are visible.
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ------------------------------------------------------------------ TMA --
 // 2D tiled bulk tensor load global -> shared (no multicast); completes on `bar`
 // with complete_tx of the box's bytes. x is the innermost coordinate (elements).
