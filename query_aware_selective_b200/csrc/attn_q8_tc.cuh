@@ -4,15 +4,16 @@
 // The formulas are those of attn_q8.cuh. Both products take the codes as the M = 128 side
 // of an 8-bit MMA straight from shared memory, without any conversion:
 //   S^T [128 keys x N] = K [128 x 128] Q^T    (A: K rows, K-major)
-//   O^T [128 dims x N] = V^T [128 x 128] W^T  (A: V rows read M-major)
+//   O^T [128 dims x N] = V^T [128 x 128] W^T  (A: V rows read M-major; B: W N-major, so a
+//                                              thread stores its key's pieces side by side)
 // kind::f8f6f4 for e4m3 (fp32 sums), kind::i8 for int8 (exact 32-bit sums). Queries and
 // weights go in as P pieces of 8 bits, each its own column:
 //   e4m3: piece p = e4m3(16^p (x - pieces before)), 4 significant bits each: two for a bf16
 //         query, three for a weight (relative 2^-13)
 //   int8: digits of 7 bits of an integer: three for a query (its row's largest is 2^19 to
 //         2^20), four for a weight (its tile's largest is 2^27)
-// so column p * RT + r is piece p of query row r, and a row's value is the sum of its
-// columns times 2^(-4 p) or 2^(-7 p).
+// and a row's value is the sum of its columns times 2^(-4 p) or 2^(-7 p). Column (rg NW + p)
+// WR + r is piece p of row r of row group rg.
 // Weights are taken relative to their key tile's own maximum (of 128 keys), and a tile's O
 // is drained from TMEM into fp32 registers and scaled there: the range of 8-bit pieces
 // then only has to span one tile (a weight is rounded to 2^-26 (e4m3) or 2^-28 (int8) of its
@@ -55,6 +56,7 @@ struct QtShape {
   static constexpr int kO = kMl + 2 * kQtMaxCluster * TG * RT, kOFloats = 160 * TG * RT;   // csize * q8_dims_per <= 160
   static constexpr uint32_t kRing = kCtrl + 256 + (kO + kOFloats) * 4;                     // list entries [stage][128]
   static constexpr uint32_t kSmem = kRing + kStages * 512;
+  static_assert((WR == 4 && RG == 1) || (WR == 8 && N - NW * RT <= 8), "columns of a weight's stores");
   static_assert(kSmem <= 232448 && (NS + 2) * N <= 512 && (kMl * 4) % 16 == 0 && (kO * 4) % 16 == 0, "does not fit an SM");
 };
 
@@ -92,34 +94,38 @@ __device__ __forceinline__ void umma_q8_elect(uint32_t d_tmem, uint32_t a_lo, ui
 }
 // Instruction descriptor: e4m3 x e4m3 -> fp32, or s8 x s8 -> s32.
 template <int FMT>
-__host__ __device__ constexpr uint32_t q8_idesc(uint32_t n, uint32_t a_mn_major) {
-  return FMT == kQ8E4M3 ? umma_idesc(0, 128, n, a_mn_major, 0)
-                        : (2u << 4) | (1u << 7) | (1u << 10) | (a_mn_major << 15) | ((n >> 3) << 17) | (8u << 24);
+__host__ __device__ constexpr uint32_t q8_idesc(uint32_t n, uint32_t mn_major) {
+  return FMT == kQ8E4M3 ? umma_idesc(0, 128, n, mn_major, mn_major)
+                        : (2u << 4) | (1u << 7) | (1u << 10) | (mn_major << 15) | (mn_major << 16) | ((n >> 3) << 17) |
+                              (8u << 24);
+}
+// Descriptor of an operand without swizzle: 8 x 16-byte core matrices, here MN-major (a row
+// of 16 bytes is 16 columns of one k): next 8 k at k_bytes, next 16 columns at mn_bytes.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t k_bytes, uint32_t mn_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((k_bytes >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((mn_bytes >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46);
 }
 
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ float redux_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// NP pieces of WR columns, RT columns apart, of a TMEM buffer (this thread's lane)
-template <int NP, int WR, int RT>
-__device__ __forceinline__ void tmem_ld_pieces(uint32_t addr, uint32_t (&v)[NP * WR]) {
+// NC columns (a multiple of 4) of a TMEM buffer, this thread's lane
+template <int NC>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&v)[NC]) {
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    if constexpr (WR == 8)
-      tmem_ld8(addr + p * RT, v + p * 8);
-    else
-      asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(v[4 * p]), "=r"(v[4 * p + 1]), "=r"(v[4 * p + 2]), "=r"(v[4 * p + 3])
-                   : "r"(addr + p * RT));
-  }
+  for (int c = 0; c + 8 <= NC; c += 8) tmem_ld8(addr + c, v + c);
+  if constexpr (NC % 8 == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[NC - 4]), "=r"(v[NC - 3]), "=r"(v[NC - 2]), "=r"(v[NC - 1])
+                 : "r"(addr + NC - 4));
   tmem_wait_ld();
 }
 __device__ __forceinline__ void st_dsmem_f32(uint32_t addr, float v) {
@@ -319,9 +325,11 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     // ------------------------------------------------------------------- MMA issuer
     // The warp runs converged and one elected lane issues (by lane 0 alone, in a branch, the
     // four MMAs and two commits of a product took 800 cycles: the pace of the whole kernel).
-    constexpr uint32_t idesc_s = q8_idesc<FMT>(N, 0), idesc_o = q8_idesc<FMT>(N, 1);
+    constexpr uint32_t idesc_s = q8_idesc<FMT>(N, 0), idesc_o = q8_idesc<FMT>(N, 1);        // (A, and with it B, MN-major)
     const uint64_t dsc = sdesc_sw128(base, 16, 1024);
     const uint32_t d_lo = (uint32_t)dsc, d_hi = (uint32_t)(dsc >> 32);     // of the start of shared memory
+    const uint64_t wsc = sdesc_plain(base + Sh::kW, 128, 2048);            // 8 keys: 128 bytes; 16 columns: 2 KB
+    const uint32_t w_lo0 = (uint32_t)wsc, w_hi = (uint32_t)(wsc >> 32);
     bool ok = nt == 0 || mbar_wait_warp(&sm.q_full, 0, abort_flag, 709);
     // Whichever is ready next: O of tile jp (its weights are written), or S of tile js (its
     // codes have landed, and js < jp + NS: the scores that were in its buffer have been read,
@@ -334,11 +342,11 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     for (uint32_t spin = 0; ok && jp < nt;) {
       if (jp < js && __all_sync(0xffffffffu, mbar_test_wait(&sm.w_full[jp & 1], (jp >> 1) & 1))) {
         tc_fence_after();
-        const uint32_t v_lo = d_lo + ((sp * kQtStage + kQtTile) >> 4), w_lo = d_lo + ((Sh::kW + (jp & 1) * N * 128) >> 4);
+        const uint32_t v_lo = d_lo + ((sp * kQtStage + kQtTile) >> 4), w_lo = w_lo0 + (((jp & 1) * N * 128) >> 4);
         const uint32_t d = tmem + (NS + (jp & 1)) * N;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)              // 32 keys: four 8-row groups of V, 32 bytes of a W row
-          umma_q8_elect<FMT>(d, v_lo + kk * 256, d_hi, w_lo + kk * 2, d_hi, idesc_o, kk > 0);
+        for (int kk = 0; kk < 4; ++kk)              // 32 keys: four 8-row groups of V and of W
+          umma_q8_elect<FMT>(d, v_lo + kk * 256, d_hi, w_lo + kk * 32, w_hi, idesc_o, kk > 0);
         umma_commit_elect(&sm.o_full[jp & 1]);
         umma_commit_elect(&sm.empty[sp]);
         ++jp;
@@ -412,25 +420,23 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
         const int d = part * DPT + e;
 #pragma unroll
         for (int p = 0; p < NW; ++p) {
-          const uint32_t n = p * RT + r;
+          const uint32_t n = (rg * NW + p) * WR + (r - row_wg);
           const uint32_t v = p < NQ ? pc[0][p < NQ ? p : 0] | (pc[1][p < NQ ? p : 0] << 16) : 0u;
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(q0 + n * 128 + (((d >> 4) ^ (n & 7)) << 4) + (d & 15)), "r"(v)
                        : "memory");
         }
       }
-      // columns that belong to no piece: zero in the queries and in both weight buffers
-      if constexpr (N > NW * RT) {
-        constexpr int pad = (N - NW * RT) * 8;          // 16-byte pieces of a buffer (W follows Q)
-        for (int z = threadIdx.x; z < 3 * pad; z += 128 * RG)
-          st_shared_v4(base + Sh::kQ + ((z / pad) * N + NW * RT) * 128 + (z % pad) * 16, 0u, 0u, 0u, 0u);
-      }
+      // columns that belong to no piece are zero
+      if constexpr (N > NW * RT)
+        for (int z = threadIdx.x; z < (N - NW * RT) * 8; z += 128 * RG)
+          st_shared_v4(q0 + NW * RT * 128 + z * 16, 0u, 0u, 0u, 0u);
       fence_proxy_async();
       mbar_arrive_warp(&sm.q_full);
     }
     asm volatile("bar.sync %0, %1;" ::"n"(kBarQ), "n"(kSoftThreads) : "memory");
 #pragma unroll
     for (int q = 0; q < WR; ++q) xs[q] = sm_xs[row_wg + q];
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + row_wg;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + rg * NW * WR;
     float al[WR], be[WR];                           // the tile's factors on o and on its own O
     auto spin_warp = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, site));
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       if (!spin_warp(&sm.o_full[j & 1], (j >> 1) & 1, 712)) return false;
       tc_fence_after();
       uint32_t v[NW * WR];
-      tmem_ld_pieces<NW, WR, RT>(lane_base + (NS + (j & 1)) * N, v);
+      tmem_ld_cols(lane_base + (NS + (j & 1)) * N, v);
 #pragma unroll
       for (int r = 0; r < WR; ++r) o[r] = fmaf(o[r], al[r], q8_join<FMT, WR, NW>(v, r) * be[r]);
       return true;
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       const float lv = __log2f(fmaxf(sc[kQtKeys + key], 0x1p-120f));
       {
         uint32_t v[NQ * WR];
-        tmem_ld_pieces<NQ, WR, RT>(lane_base + (j % NS) * N, v);
+        tmem_ld_cols(lane_base + (j % NS) * N, v);
 #pragma unroll
         for (int r = 0; r < WR; ++r) x[r] = fmaf(q8_join<FMT, WR, NQ>(v, r), ka * xs[r], lv);
       }
@@ -467,11 +473,13 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       }
       // the tile's maximum of each row
       float mt[WR];
-      float* mx = smf + Sh::kMax + (j & 1) * 4 * RT + row_wg;
+      float4* mx = reinterpret_cast<float4*>(smf + Sh::kMax + (j & 1) * 4 * RT + row_wg);      // [warp][RT]
 #pragma unroll
-      for (int r = 0; r < WR; ++r) {
-        mt[r] = redux_max(x[r]);
-        if (lane == 0) mx[(warp & 3) * RT + r] = mt[r];
+      for (int r = 0; r < WR; ++r) mt[r] = redux_max(x[r]);
+      if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < WR; r += 4)
+          mx[((warp & 3) * RT + r) / 4] = make_float4(mt[r], mt[r + 1], mt[r + 2], mt[r + 3]);
       }
       // the O of this warpgroup's tile before (PV_j will overwrite it if TG is 2, and the W
       // buffer below was its own)
@@ -479,22 +487,36 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       // a named barrier has no time limit: the four warps leave together if a wait ran out
       if (!(ok = bar_all(bar_wg, 128, ok))) break;
 #pragma unroll
-      for (int r = 0; r < WR; ++r)
-        mt[r] = fmaxf(fmaxf(mx[r], mx[RT + r]), fmaxf(mx[2 * RT + r], mx[3 * RT + r]));
-      // weights, as pieces, to row p * RT + r of the W buffer, byte `key`
-      const uint32_t wb = base + Sh::kW + (j & 1) * N * 128 + row_wg * 128 + (key & 15);
+      for (int r = 0; r < WR; r += 4) {
+        const float4 m0 = mx[r / 4], m1 = mx[(RT + r) / 4], m2 = mx[(2 * RT + r) / 4], m3 = mx[(3 * RT + r) / 4];
+        mt[r] = fmaxf(fmaxf(m0.x, m1.x), fmaxf(m2.x, m3.x));
+        mt[r + 1] = fmaxf(fmaxf(m0.y, m1.y), fmaxf(m2.y, m3.y));
+        mt[r + 2] = fmaxf(fmaxf(m0.z, m1.z), fmaxf(m2.z, m3.z));
+        mt[r + 3] = fmaxf(fmaxf(m0.w, m1.w), fmaxf(m2.w, m3.w));
+      }
+      // weights, as pieces, to this key's row of the W buffer: [16 columns][128 keys][16 bytes]
       const float iv = fast_exp2(-lv - kTop);
+      uint32_t ww[NW + 1][WR / 4];
 #pragma unroll
-      for (int r = 0; r < WR; r += 2) {
-        uint32_t pc[NW];
-        x[r] = fast_exp2(x[r] - (mt[r] == -INFINITY ? 0.f : mt[r]) + kTop);
-        x[r + 1] = fast_exp2(x[r + 1] - (mt[r + 1] == -INFINITY ? 0.f : mt[r + 1]) + kTop);
-        q8_split2<FMT, NW>(x[r], x[r + 1], pc);
+      for (int r = 0; r < WR; r += 4) {
+        uint32_t lo[NW], hi[NW];
 #pragma unroll
-        for (int p = 0; p < NW; ++p) {
-          const uint32_t n0 = p * RT + r, n1 = n0 + 1;           // (row_wg is a multiple of 8, or 0)
-          st_shared_u8(wb + n0 * 128 + (((key >> 4) ^ (n0 & 7)) << 4), pc[p]);
-          st_shared_u8(wb + n1 * 128 + (((key >> 4) ^ (n1 & 7)) << 4), pc[p] >> 8);
+        for (int u = 0; u < 4; ++u) x[r + u] = fast_exp2(x[r + u] - (mt[r + u] == -INFINITY ? 0.f : mt[r + u]) + kTop);
+        q8_split2<FMT, NW>(x[r], x[r + 1], lo);
+        q8_split2<FMT, NW>(x[r + 2], x[r + 3], hi);
+#pragma unroll
+        for (int p = 0; p < NW; ++p) ww[p][r / 4] = __byte_perm(lo[p], hi[p], 0x5410);
+        ww[NW][r / 4] = 0u;
+      }
+      const uint32_t wb = base + Sh::kW + (j & 1) * N * 128 + key * 16;
+      if constexpr (WR == 4) {
+        st_shared_v4(wb, ww[0][0], ww[1][0], ww[2][0], NW == 4 ? ww[3][0] : 0u);
+      } else {
+        // (the last row group's pieces are followed by the columns that belong to none)
+#pragma unroll
+        for (int p = 0; p < NW + (N > NW * RT ? 1 : 0); ++p) {
+          const int col = (rg * NW + p) * WR;
+          if (p < NW || rg == RG - 1) st_shared_v2(wb + (col >> 4) * 2048 + (col & 15), ww[p][0], ww[p][WR / 4 - 1]);
         }
       }
       fence_proxy_async();
