@@ -1,6 +1,7 @@
-// attn_q8.cuh - exact attention of few queries over the initial + selected + local tokens
-// of an 8-bit cache (ESA write-up: implementation and final-attention paragraphs - global
-// part = initial + selected tokens, window part = local tokens, one softmax).
+// attn_q8.cuh - exact attention over the initial + selected + local tokens of an 8-bit cache
+// for fp32 queries and for heads of 64 (ESA write-up: implementation and final-attention
+// paragraphs - global part = initial + selected tokens, window part = local tokens, one
+// softmax). bf16 queries on heads of 128 run attn_q8_tc.cuh.
 //
 // With codes kc, vc and block scales a, b the logits and the output of a query row are
 //   x_j = c (q . kc_j) a_j,    l = sum_j 2^(x_j - m),    o = sum_j 2^(x_j + log2 b_j - m) vc_j / l
@@ -12,20 +13,26 @@
 // Keys and dims are the M dimension and the query rows N = 8, because a decode step has
 // only the G heads of a KV head as rows. A dot product does not mind the order of its
 // terms, so the fragments take their dims (K) and keys (V) in the order in which 16-byte
-// loads from global memory deliver them: no shared memory and no transposition in the
-// loop, only byte pairs of two keys brought side by side (prmt) and one conversion per
-// two codes. S^T becomes the B operand of the second product by movmatrix.
+// shared-memory loads deliver them: no transposition but byte pairs of two keys brought
+// side by side (prmt), and one conversion per two codes. S^T becomes the B operand of the
+// second product by movmatrix.
 // m is a reference, not the maximum: it is raised to max_j (x_j + log2 b_j) when that
 // exceeds it by 5, and W = 2^(x_j + log2 b_j - m + 10) <= 2^15 is rounded to f16 (relative
 // 2^-11; a weight under 2^-35 of the largest is lost, which 2^20 of them do not make
-// visible). l sums the unrounded W 2^-10 / b_j. fp32 queries go in as two f16 (q = hi + lo), and so do the
-// weights, for 22 bits of each.
+// visible). l sums the unrounded W 2^-10 / b_j. fp32 queries go in as two f16 (q = hi +
+// lo), and so do the weights, for 22 bits of each: more bits than 8-bit pieces give in a
+// narrow MMA, which is why fp32 stays here; a head of 64 is half the M = 128 that the
+// 8-bit MMAs of attn_q8_tc.cuh take.
 //
-// Bound by HBM: each attended code is read once. A warp streams 16 keys a step, 16 bytes a
-// lane and load, the next step's codes in flight under the present one's arithmetic. The
-// key list of a (sequence, KV head) is split over the warps of a CTA and over the CTAs of
-// a cluster; the parts meet in (distributed) shared memory, so there is no workspace, no
-// counter to clear and no second kernel.
+// Bound by HBM for large batches (bf16, heads of 64, 16 sequences x 6.3K keys x 8 heads,
+// 103 MB: 32 us, 3.2 TB/s), by the conversions' and the softmax's issue slots for fp32 on
+// heads of 128 (206 MB: 53 us), by latency for one short sequence (4 heads of 64, 400 keys:
+// 5 us, of which 2 are the launch). A warp streams 16 keys a step through its own ring of
+// three steps in shared memory (16-byte cp.async). The key list of a (sequence, KV head) is
+// split over the 8 warps of a CTA and over the CTAs of a cluster; the parts meet in
+// (distributed) shared memory, so there is no workspace, no counter to clear and no second
+// kernel. (A CTA per KV head; several heads in one, for longer consecutive reads, measured
+// the same or slower: 32.0, 32.5, 33.3 us for 1, 2, 4 heads at 256 CTAs.)
 #pragma once
 #include "attn_tc.cuh"
 #include "cache_q8.cuh"
@@ -51,7 +58,6 @@ struct AttnQ8Args {
   int64_t n_cap, nblk, c0;
   int lq, hq, hkv, G;
   int lists, bshift;
-  int hc;                   // KV heads of a CTA (1, 2, 4 or 8; divides hkv)
   int tiles;                // row tiles of a KV head
   float scale_log2;
 };
@@ -169,9 +175,9 @@ __device__ __forceinline__ void load4(const T* p, float* f) {
   }
 }
 
-// grid (cluster size, (Hkv / hc) * tiles, B), cluster (cluster size, 1, 1).
+// grid (cluster size, Hkv * tiles, B), cluster (cluster size, 1, 1).
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1) attn_q8_kernel(const AttnQ8Args a) {
+__global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q8_kernel(const AttnQ8Args a) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int ROWS = 8 * NT;
   constexpr int KC = D / 64;             // 16-byte pieces of a key row a lane takes (K)
@@ -180,14 +186,11 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   extern __shared__ __align__(128) float q8sm[];
   float* const sm_o = q8sm;                                    // [warp][ROWS][RF]
   float* const sm_ml = sm_o + kQ8Warps * ROWS * RF;            // [warp][ROWS][2]
-  float* const sm_fin = sm_ml + 2 * kQ8Warps * ROWS;           // [head slot][ROWS][2]
+  float* const sm_fin = sm_ml + 2 * kQ8Warps * ROWS;           // [ROWS][2]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  const int hc = a.hc, kw = kQ8Warps / hc;
-  const int hs = warp & (hc - 1), kp = warp / hc;
-  const int hg = blockIdx.y / a.tiles, tile = blockIdx.y - hg * a.tiles;
-  const int g = hg * hc + hs, b = blockIdx.z;
+  const int g = blockIdx.y / a.tiles, tile = blockIdx.y - g * a.tiles, b = blockIdx.z;
   const int rank = blockIdx.x, csize = gridDim.x;
 
   const int list = a.lists > 1 ? b * a.lists + g : b;
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   const int n_all = n_prior + i_first + 1;                     // that every row of the tile attends
   const int steps = (n_keys + kQ8Keys - 1) / kQ8Keys;
   // the warps' shares of the steps interleave: each gets its part of the scattered keys
-  const int s_beg = rank * kw + kp, s_end = steps, s_inc = csize * kw;
+  const int s_beg = rank * kQ8Warps + warp, s_end = steps, s_inc = csize * kQ8Warps;
 
   // ---- the stream: the warp's own ring of kQ8Stages steps in shared memory, filled by
   // 16-byte cp.async (8 or 4 lanes a row), positions looked up one step before that
@@ -480,31 +483,33 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       if (gid == 0) *reinterpret_cast<float2*>(sm_ml + (warp * ROWS + r) * 2) = make_float2(m[nt][j], l[nt][j]);
     }
   __syncthreads();
-  // merge the key parts of each head inside the CTA: slot hs takes over warps hs + hc * kp
+  // merge the warps of the CTA, into the first one's rows
   constexpr int Q = D / 4;
-  for (int it = threadIdx.x; it < hc * nrow * Q; it += kQ8Threads) {
-    const int d4 = it % Q, r = (it / Q) % nrow, h = it / Q / nrow;
+  for (int it = threadIdx.x; it < nrow * Q; it += kQ8Threads) {
+    const int d4 = it % Q, r = it / Q;
     float M = -INFINITY;
-    for (int u = 0; u < kw; ++u) M = fmaxf(M, sm_ml[((h + hc * u) * ROWS + r) * 2]);
+#pragma unroll
+    for (int u = 0; u < kQ8Warps; ++u) M = fmaxf(M, sm_ml[(u * ROWS + r) * 2]);
     const float mr = M == -INFINITY ? 0.f : M;
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int u = 0; u < kw; ++u) {
-      const int wr = (h + hc * u) * ROWS + r;
+#pragma unroll
+    for (int u = 0; u < kQ8Warps; ++u) {
+      const int wr = u * ROWS + r;
       const float c = fast_exp2(sm_ml[wr * 2] - mr);
       const float4 o = *reinterpret_cast<const float4*>(sm_o + wr * RF + d4 * 4);
       L += sm_ml[wr * 2 + 1] * c;
       O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
     }
-    *reinterpret_cast<float4*>(sm_o + (h * ROWS + r) * RF + d4 * 4) = O;     // read by this thread only
-    if (d4 == 0) *reinterpret_cast<float2*>(sm_fin + (h * ROWS + r) * 2) = make_float2(M, L);
+    *reinterpret_cast<float4*>(sm_o + r * RF + d4 * 4) = O;                  // read by this thread only
+    if (d4 == 0) *reinterpret_cast<float2*>(sm_fin + r * 2) = make_float2(M, L);
   }
   if (csize > 1) cluster_sync_all();
   else __syncthreads();
   // merge the CTAs of the cluster: CTA `rank` writes every csize-th group of 256 items
-  for (int it = threadIdx.x + kQ8Threads * rank; it < hc * nrow * Q; it += kQ8Threads * csize) {
-    const int d4 = it % Q, r = (it / Q) % nrow, h = it / Q / nrow;
-    const uint32_t ml = smem_u32(sm_fin + (h * ROWS + r) * 2), oo = smem_u32(sm_o + (h * ROWS + r) * RF + d4 * 4);
+  for (int it = threadIdx.x + kQ8Threads * rank; it < nrow * Q; it += kQ8Threads * csize) {
+    const int d4 = it % Q, r = it / Q;
+    const uint32_t ml = smem_u32(sm_fin + r * 2), oo = smem_u32(sm_o + r * RF + d4 * 4);
     float M = -INFINITY;
     for (int u = 0; u < csize; ++u) M = fmaxf(M, __uint_as_float(ld_dsmem_u32(dsmem_map(ml, u))));
     const float mr = M == -INFINITY ? 0.f : M;
@@ -517,8 +522,8 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       L += __uint_as_float(z.y) * c;
       O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
     }
-    const int i = (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
-    const int64_t row = ((int64_t)b * a.lq + i) * a.hq + (hg * hc + h) * a.G + hl;
+    const int i = a.lq == 1 ? 0 : (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
+    const int64_t row = ((int64_t)b * a.lq + i) * a.hq + g * a.G + hl;
     const float inv = 0x1p-10f / L;                                          // 2^-kQ8Head
     T* dst = static_cast<T*>(a.o) + row * D + d4 * 4;
     if constexpr (F32) {

@@ -176,7 +176,7 @@ __device__ __forceinline__ void q8_split2(float x0, float x1, uint32_t* pc) {
 // Dims that each CTA of a cluster merges, a multiple of 4 (the last CTA the rest, if any).
 __device__ __forceinline__ int q8_dims_per(int csize) { return ((128 + csize - 1) / csize + 3) & ~3; }
 
-// grid (cluster size, Hkv * tiles, B), cluster (cluster size, 1, 1); a.hc = 1.
+// grid (cluster size, Hkv * tiles, B), cluster (cluster size, 1, 1).
 template <int FMT, int WR, int RG, int TG>
 __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_q8_tc_kernel(const AttnQ8Args a) {
   using Sh = QtShape<FMT, WR, RG, TG>;

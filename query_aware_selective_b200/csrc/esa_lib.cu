@@ -1298,68 +1298,21 @@ int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
   return cdiv(r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq, esa::kTcKeys) * esa::kTcKeys;
 }
 
-// How a few-query call is spread: hc KV heads per CTA (its 8 warps split each head's keys
-// 8 / hc ways) and clusters of csize CTAs per unit of work, aiming at two CTAs on each of
-// the 148 SMs with at least one step of keys per warp.
-struct Q8Plan {
-  int hc, csize;
-};
-Q8Plan plan_q8(int64_t batch, int64_t tiles, int hkv, int64_t n_keys) {
-  const int64_t slots = 2 * 148, steps = cdiv(n_keys, esa::kQ8Keys);
-  Q8Plan best{1, 1};
-  int64_t best_ctas = 0;
-  for (int hc = 8; hc >= 1; hc /= 2) {
-    if (hkv % hc) continue;
-    const int64_t units = batch * tiles * (hkv / hc), kw = esa::kQ8Warps / hc;
-    const int64_t c = std::max<int64_t>(1, std::min<int64_t>({8, slots / units, cdiv(steps, kw)}));
-    const int64_t ctas = std::min<int64_t>(units * c, slots);
-    if (ctas > best_ctas) {
-      best_ctas = ctas;
-      best = Q8Plan{hc, (int)c};
-    }
-  }
-  return best;
-}
-
-template <typename T, int D, int FMT, int NT>
-esa_status_t launch_attn_q8(const esa::AttnQ8Args& a, dim3 grid, int csize, cudaStream_t s) {
-  constexpr int smem = esa::q8_smem_bytes<NT, D>();
-  static const char what = 0;
-  const esa_status_t st =
-      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_kernel<T, D, FMT, NT>, smem); });
-  if (st != ESA_OK) return st;
-  const esa_status_t ls = launch_q8(esa::attn_q8_kernel<T, D, FMT, NT>, "attn_q8_kernel", grid, esa::kQ8Threads, smem,
-                                    csize, s, a);
-  return ls == ESA_OK ? ok() : ls;
-}
-template <typename T, int D>
-esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int nt, dim3 grid, int csize, cudaStream_t s) {
-  if (format == ESA_Q8_E4M3)
-    return nt == 1 ? launch_attn_q8<T, D, esa::kQ8E4M3, 1>(a, grid, csize, s)
-                   : launch_attn_q8<T, D, esa::kQ8E4M3, 2>(a, grid, csize, s);
-  return nt == 1 ? launch_attn_q8<T, D, esa::kQ8Int8, 1>(a, grid, csize, s)
-                 : launch_attn_q8<T, D, esa::kQ8Int8, 2>(a, grid, csize, s);
-}
-
-template <int FMT, int WR, int RG, int TG>
-esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cudaStream_t s) {
-  using Sh = esa::QtShape<FMT, WR, RG, TG>;
-  static const char what = 0;
-  const esa_status_t st =
-      once_per_context(&what, [] { return set_max_smem(esa::attn_q8_tc_kernel<FMT, WR, RG, TG>, Sh::kSmem); });
-  if (st != ESA_OK) return st;
-  a.tiles = (int)cdiv((int64_t)a.lq * a.G, Sh::RT);
-  if ((int64_t)a.hkv * a.tiles > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
-  // How many clusters of 2 .. 8 CTAs fit the GPU at once (a byte each; the SMs of a GPC do not
-  // divide by every size: 24 clusters of 6 CTAs of one per SM left 8 CTAs to a second wave).
-  static const char fits = 0;
+// The largest cluster of up to 8 CTAs (and up to `most`) with which `units` units of work, a
+// cluster each, all run at once: clusters split a unit's keys, a second wave would cost
+// what they save (24 units x 6 CTAs of one per SM left 8 CTAs to a second wave, 44 against
+// 25 us; fp32 on 128 units, one CTA per SM: 53 us without clusters, 60 with two CTAs). How
+// many clusters of 2 .. 8 fit is asked once per kernel and context (a byte each).
+template <typename Kernel>
+esa_status_t q8_cluster_size(Kernel kernel, int threads, int smem, int64_t units, int64_t most, int* csize) {
   intptr_t fit = 0;
-  const esa_status_t qs = per_context(&fits, &fit, [](intptr_t* v) {
-    for (int c = 2; c <= esa::kQtMaxCluster; ++c) {
+  const esa_status_t st = per_context(reinterpret_cast<const void*>(kernel), &fit, [&](intptr_t* v) {
+    ESA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    for (int c = 2; c <= 8; ++c) {
       cudaLaunchConfig_t q = {};
       q.gridDim = dim3(c);
-      q.blockDim = dim3(Sh::kThreads);
-      q.dynamicSmemBytes = Sh::kSmem;
+      q.blockDim = dim3(threads);
+      q.dynamicSmemBytes = smem;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
       at[0].val.clusterDim.x = c;
@@ -1368,21 +1321,55 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
       q.attrs = at;
       q.numAttrs = 1;
       int n = 0;
-      ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, esa::attn_q8_tc_kernel<FMT, WR, RG, TG>, &q));
+      ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &q));
       *v |= (intptr_t)std::min(n, 255) << (8 * (c - 2));
     }
     return ESA_OK;
   });
-  if (qs != ESA_OK) return qs;
-  // the largest cluster with which every unit of work still runs at once
-  const int64_t units = (int64_t)batch * a.hkv * a.tiles, tiles = cdiv(n_keys, esa::kQtKeys);
-  int csize = 1;
-  for (int c = 2; c <= esa::kQtMaxCluster && c <= tiles; ++c)
-    if (units <= ((fit >> (8 * (c - 2))) & 255)) csize = c;
-  const esa_status_t ls =
-      launch_q8(esa::attn_q8_tc_kernel<FMT, WR, RG, TG>, "attn_q8_tc_kernel", dim3(csize, a.hkv * a.tiles, batch),
-                Sh::kThreads, Sh::kSmem, csize, s, a);
-  return ls == ESA_OK ? ok() : ls;
+  if (st != ESA_OK) return st;
+  *csize = 1;
+  for (int c = 2; c <= 8 && c <= most; ++c)
+    if (units <= ((fit >> (8 * (c - 2))) & 255)) *csize = c;
+  return ESA_OK;
+}
+
+template <typename T, int D, int FMT, int NT>
+esa_status_t launch_attn_q8(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cudaStream_t s) {
+  auto* kernel = esa::attn_q8_kernel<T, D, FMT, NT>;
+  constexpr int smem = esa::q8_smem_bytes<NT, D>();
+  const int64_t tiles = cdiv((int64_t)a.lq * a.G, 8 * NT);
+  if (tiles * a.hkv > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
+  a.tiles = (int)tiles;
+  int csize;
+  esa_status_t st = q8_cluster_size(kernel, esa::kQ8Threads, smem, (int64_t)batch * a.hkv * tiles,
+                                    cdiv(n_keys, esa::kQ8Keys * esa::kQ8Warps), &csize);
+  if (st != ESA_OK) return st;
+  st = launch_q8(kernel, "attn_q8_kernel", dim3(csize, a.hkv * a.tiles, batch), esa::kQ8Threads, smem, csize, s, a);
+  return st == ESA_OK ? ok() : st;
+}
+template <typename T, int D>
+esa_status_t dispatch_attn_q8(const esa::AttnQ8Args& a, int format, int32_t batch, int64_t n_keys, cudaStream_t s) {
+  const bool one = (int64_t)a.lq * a.G <= 8;        // tiles of 8 or 16 query rows
+  if (format == ESA_Q8_E4M3)
+    return one ? launch_attn_q8<T, D, esa::kQ8E4M3, 1>(a, batch, n_keys, s)
+               : launch_attn_q8<T, D, esa::kQ8E4M3, 2>(a, batch, n_keys, s);
+  return one ? launch_attn_q8<T, D, esa::kQ8Int8, 1>(a, batch, n_keys, s)
+             : launch_attn_q8<T, D, esa::kQ8Int8, 2>(a, batch, n_keys, s);
+}
+
+template <int FMT, int WR, int RG, int TG>
+esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cudaStream_t s) {
+  using Sh = esa::QtShape<FMT, WR, RG, TG>;
+  auto* kernel = esa::attn_q8_tc_kernel<FMT, WR, RG, TG>;
+  const int64_t tiles = cdiv((int64_t)a.lq * a.G, Sh::RT);
+  if (tiles * a.hkv > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
+  a.tiles = (int)tiles;
+  int csize;
+  esa_status_t st = q8_cluster_size(kernel, Sh::kThreads, Sh::kSmem, (int64_t)batch * a.hkv * tiles,
+                                    cdiv(n_keys, esa::kQtKeys), &csize);
+  if (st != ESA_OK) return st;
+  st = launch_q8(kernel, "attn_q8_tc_kernel", dim3(csize, a.hkv * a.tiles, batch), Sh::kThreads, Sh::kSmem, csize, s, a);
+  return st == ESA_OK ? ok() : st;
 }
 // Rows in as few equal tiles as 24 rows allow, and the warpgroups that hold such a tile.
 template <int FMT>
@@ -1475,7 +1462,7 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
   const float sl2 = scale * 1.4426950408889634f;
   const Regions r = regions(c0, p);
   // positions in a key list are 32-bit (counts are clamped to topk on the device)
-  if (r.ni + (int64_t)p.topk + (c0 - r.lo) + lq >= ((int64_t)1 << 31) - 64)
+  if (r.ni + (int64_t)p.topk + (c0 - r.lo) + lq >= ((int64_t)1 << 31) - 65536)
     return fail(ESA_ERR_UNSUPPORTED, "a key list of 2^31 tokens or more");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   esa::KeyList keys{idx, p.topk, r.ni, r.lo, c.n_cap, count};
@@ -1487,7 +1474,6 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
     return attn_q8_chunk(q, c, lq, c0, hq, keys, lists, p, sl2, o, lse, workspace, s);
   }
   const int g = hq / c.hkv;
-  const int64_t rows = (int64_t)lq * g;
   const int64_t n_keys = r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq;
   esa::AttnQ8Args a{};
   a.q = q;
@@ -1511,17 +1497,9 @@ esa_status_t sparse_attn_q8_impl(const void* q, esa_dtype_t dt, const esa_cache_
   if (dt == ESA_BF16 && c.head_dim == 128)
     return c.format == ESA_Q8_E4M3 ? dispatch_attn_q8_tc<esa::kQ8E4M3>(a, c.batch, n_keys, s)
                                    : dispatch_attn_q8_tc<esa::kQ8Int8>(a, c.batch, n_keys, s);
-  // fp32 queries (22 bits of them and of the weights) and heads of 64
-  const int nt = rows <= 8 ? 1 : 2;
-  const int64_t tiles = cdiv(rows, 8 * nt);
-  const Q8Plan pl = plan_q8(c.batch, tiles, c.hkv, n_keys);
-  if (tiles * (c.hkv / pl.hc) > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
-  a.hc = pl.hc;
-  a.tiles = (int)tiles;
-  const dim3 grid((unsigned)pl.csize, (unsigned)(tiles * (c.hkv / pl.hc)), c.batch);
-  if (dt == ESA_BF16) return dispatch_attn_q8<__nv_bfloat16, 64>(a, c.format, nt, grid, pl.csize, s);
-  return c.head_dim == 128 ? dispatch_attn_q8<float, 128>(a, c.format, nt, grid, pl.csize, s)
-                           : dispatch_attn_q8<float, 64>(a, c.format, nt, grid, pl.csize, s);
+  if (dt == ESA_BF16) return dispatch_attn_q8<__nv_bfloat16, 64>(a, c.format, c.batch, n_keys, s);
+  return c.head_dim == 128 ? dispatch_attn_q8<float, 128>(a, c.format, c.batch, n_keys, s)
+                           : dispatch_attn_q8<float, 64>(a, c.format, c.batch, n_keys, s);
 }
 
 }  // namespace
