@@ -421,7 +421,8 @@ typedef struct {
  * qmax 448 or 127). New rows become round(x / s'), the block's rows before `start`
  * round(code * s / s') where s' > s (nearest, ties to even). Both divisions are by a power
  * of two, so codes and values are defined to the bit. Rows at or behind start + rows keep
- * their codes and count as empty: a later write there decides the scale again.
+ * their codes and count as empty: a later write there decides the scale again. (A scale
+ * found there that is not a positive finite number counts as 0.)
  *   k, v: rows of [hkv, head_dim], dtype dt (ESA_F32 or ESA_BF16); row r of sequence b at
  *         element b * batch_stride + r * row_stride (each row contiguous; strides give
  *         16-byte aligned rows, so slices of a fused projection can be passed)
@@ -459,7 +460,9 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  *   q, o:       [batch, lq, hq, head_dim] of dtype dt (ESA_F32 or ESA_BF16)
  *   idx, count: [batch, lists, p.topk] and [batch, lists] int32, as the selections write them
  *   lse:        NULL or [batch, lq, hq] fp32
- * Scales may be any positive numbers below 2^121. hq is a multiple of hkv; no limit on
+ * Scales may be any positive numbers below 2^121, and the codes of attended keys any but
+ * e4m3's NaN (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a
+ * row of NaN. hq is a multiple of hkv; no limit on
  * their ratio. Codes are exact in the products; softmax weights keep 11 bits or more (22
  * for fp32), and 2^-26 of the largest at least. A large chunk (bf16, head_dim 128, hq / hkv in {1, 2, 4, 8}) dequantises its
  * keys and values into the workspace as bf16 (exact for scales that are powers of two) and

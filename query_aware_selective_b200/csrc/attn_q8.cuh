@@ -156,8 +156,12 @@ __device__ __forceinline__ void q8_transpose(uint32_t wa, uint32_t wb, uint32_t*
   }
 }
 
-// A power of two f (and its reciprocal's log2) that brings amax to [2^13, 2^14): queries
-// of any range fit f16, and the elements that matter stay normal there.
+// log2 of a value block's scale (within 2^-23 at powers of two; the weights' reciprocal
+// factors are taken from it). Scales under 2^-120, zero among them, count as 2^-120.
+__device__ __forceinline__ float q8_scale_log2(float s) { return __log2f(s < 0x1p-120f ? 0x1p-120f : s); }
+
+// The exponent of a power of two that brings amax to [2^13, 2^14): queries of any range
+// fit f16, and the elements that matter stay normal there.
 __device__ __forceinline__ int q8_query_exp(float amax) {
   const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
   return min(13 - e, 100);
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
     // them says that m has to rise (at once on the first step: m is -inf).
     float ka[2], lv[2];
     {
-      const float lg = __log2f(fmaxf(sc_cur, 0x1p-120f));      // within 2^-23 at powers of two; iv follows it
+      const float lg = q8_scale_log2(sc_cur);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         ka[u] = __shfl_sync(0xffffffffu, sc_cur, gid + 8 * u);

@@ -49,13 +49,15 @@ struct QtShape {
   static constexpr int NS = 6 * N <= 512 ? 4 : 2;             // score buffers in TMEM (O: two behind them)
   static constexpr uint32_t kCols = (NS + 2) * N <= 128 ? 128 : (NS + 2) * N <= 256 ? 256 : 512;   // TMEM columns
   static constexpr uint32_t kQ = kStages * kQtStage, kW = kQ + N * 128, kCtrl = kW + 2 * N * 128;
-  // behind the control block, in floats: tile maxima [2][4][RT], logit factors [RT], l of
+  // behind the control block, in floats: tile maxima [TG][2][4][RT], logit factors [RT], l of
   // each warp [TG][4][RT], and what the warpgroups of the cluster's CTAs send: (m, l)
   // [8 TG][RT][2], o [RT][csize TG][dims of this CTA]
-  static constexpr int kMax = 0, kXs = 8 * RT, kL = 9 * RT, kMl = kL + 4 * TG * RT + (RT & 4 ? 4 : 0);
+  static constexpr int kMax = 0, kXs = 8 * TG * RT, kL = kXs + RT, kMl = kL + 4 * TG * RT + (RT & 4 ? 4 : 0);
   static constexpr int kO = kMl + 2 * kQtMaxCluster * TG * RT, kOFloats = 160 * TG * RT;   // csize * q8_dims_per <= 160
   static constexpr uint32_t kRing = kCtrl + 256 + (kO + kOFloats) * 4;                     // list entries [stage][128]
   static constexpr uint32_t kSmem = kRing + kStages * 512;
+  // a warpgroup sees every phase of the barriers it waits for
+  static_assert(kStages % TG == 0 && NS % TG == 0 && 2 % TG == 0, "stages and buffers that the tile groups share");
   static_assert((WR == 4 && RG == 1) || (WR == 8 && N - NW * RT <= 8), "columns of a weight's stores");
   static_assert(kSmem <= 232448 && (NS + 2) * N <= 512 && (kMl * 4) % 16 == 0 && (kO * 4) % 16 == 0, "does not fit an SM");
 };
@@ -398,19 +400,21 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       const __nv_bfloat16* qp =
           static_cast<const __nv_bfloat16*>(a.q) + (((int64_t)b * a.lq + i) * a.hq + g * a.G + hl) * 128 + part * DPT;
       float f[DPT];
-      float mx = 0.f;
+      uint32_t mx = 0;                              // largest magnitude, as bits (in the order of the values)
 #pragma unroll
       for (int e = 0; e < DPT; e += 4) {
         load4(qp + e, f + e);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx = fmaxf(mx, fabsf(f[e + u]));
+        for (int u = 0; u < 4; ++u) mx = max(mx, __float_as_uint(f[e + u]) & 0x7fffffffu);
       }
 #pragma unroll
-      for (int w = TPR < 32 ? TPR / 2 : 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-      // 2^qe brings the row's largest to [2^7, 2^8) (e4m3) or [2^19, 2^20) (int8)
-      const int qe = min((FMT == kQ8E4M3 ? 7 : 19) - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127), 100);
+      for (int w = TPR < 32 ? TPR / 2 : 16; w > 0; w >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      // 2^qe brings the row's largest to [2^7, 2^8) (e4m3) or [2^19, 2^20) (int8). Pieces hold no
+      // infinity (nor, as digits, NaN): a row with one gets a factor of NaN.
+      const int qe = min((FMT == kQ8E4M3 ? 7 : 19) - ((int)(mx >> 23) - 127), 100);
       const float up = __uint_as_float((uint32_t)(qe + 127) << 23);
-      if (part == 0) sm_xs[r] = a.scale_log2 * kUnitQ * __uint_as_float((uint32_t)(127 - qe) << 23);
+      if (part == 0)
+        sm_xs[r] = mx >= 0x7f800000u ? NAN : a.scale_log2 * kUnitQ * __uint_as_float((uint32_t)(127 - qe) << 23);
       const uint32_t q0 = base + Sh::kQ;
 #pragma unroll
       for (int e = 0; e < DPT; e += 4) {
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       float x[WR];
       const float* sc = reinterpret_cast<const float*>(qtsm + (j % NST) * kQtStage + 2 * kQtTile);
       const float ka = sc[key];
-      const float lv = __log2f(fmaxf(sc[kQtKeys + key], 0x1p-120f));
+      const float lv = q8_scale_log2(sc[kQtKeys + key]);
       {
         uint32_t v[NQ * WR];
         tmem_ld_cols(lane_base + (j % NS) * N, v);
@@ -473,7 +477,9 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       }
       // the tile's maximum of each row
       float mt[WR];
-      float4* mx = reinterpret_cast<float4*>(smf + Sh::kMax + (j & 1) * 4 * RT + row_wg);      // [warp][RT]
+      // [warp][RT]; two buffers in turn: a warp that writes one has passed the barrier of the
+      // tile in between, and with it every warp's reads of the maxima before that
+      float4* mx = reinterpret_cast<float4*>(smf + Sh::kMax + (2 * tg + ((j / TG) & 1)) * 4 * RT + row_wg);
 #pragma unroll
       for (int r = 0; r < WR; ++r) mt[r] = redux_max(x[r]);
       if (lane == 0) {

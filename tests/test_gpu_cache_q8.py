@@ -542,6 +542,36 @@ def test_attention_index_list_outside_the_cache_is_clamped():
         _check(o, lse, _reference(q, kv, vv, [n_cap - 1], as_read, used, 8, 64), torch.bfloat16, d)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,d,lq", [(torch.bfloat16, 128, 1), (torch.bfloat16, 128, 3), (torch.bfloat16, 64, 3),
+                                        (torch.float32, 128, 1), (torch.bfloat16, 128, 460)])
+def test_attention_nan_and_infinity_stay_in_their_rows(fmt, dtype, d, lq):
+    """A query row with a NaN or an infinity gives NaN there and nowhere else; so does the NaN
+    scale of an attended block, in its head."""
+    n_cap, hq, hkv, block = 900, 8, 2, 32
+    c0 = n_cap - lq
+    p = qas.params(16, 100, 40, 0)
+    idx, cnt = _lists([c0], 1, 16, 100, 40, 661, short=False)
+    args = (c0, idx.to(DEV), cnt.to(DEV), p)
+    cache, _, _ = _filled(1, n_cap, hkv, d, fmt, block, [n_cap], 671)
+    q = _rand((1, lq, hq, d), 681, dtype).to(DEV)
+    good, good_lse = qas.sparse_attn_q8(q, cache, *args, want_lse=True)
+    for i, h, value in ((0, 5, float("nan")), (lq - 1, 2, float("inf")), (0, 0, float("-inf"))):
+        bad = q.clone()
+        bad[0, i, h, 7] = value
+        o, lse = qas.sparse_attn_q8(bad, cache, *args, want_lse=True)
+        assert o[0, i, h].isnan().all() and lse[0, i, h].isnan()
+        o[0, i, h], lse[0, i, h] = good[0, i, h], good_lse[0, i, h]
+        assert torch.equal(o, good) and torch.equal(lse, good_lse)
+    for scale in (cache.k_scale, cache.v_scale):
+        was = scale[0, 0, 1].clone()               # the initial tokens of head 1: every query attends them
+        scale[0, 0, 1] = float("nan")
+        o, _ = qas.sparse_attn_q8(q, cache, *args)
+        assert o[0, :, hq // 2:].isnan().all() and torch.equal(o[0, :, :hq // 2], good[0, :, :hq // 2])
+        scale[0, 0, 1] = was
+    qas.device_status()
+
+
 def test_offsets_past_32_bits():
     # 3 sequences of 1M rows of 1 KB: the last ones lie past 2^31 bytes of each operand
     b, n_cap, hq, hkv, d, block = 3, 1 << 20, 32, 8, 128, 64
