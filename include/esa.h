@@ -399,7 +399,7 @@ size_t esa_sparse_attn_varlen_workspace_size(int32_t batch, int64_t n_cap, int32
  *   format:           ESA_Q8_E4M3 (4 exponent and 3 mantissa bits, +-448) or
  *                     ESA_Q8_INT8 (-127 .. 127)
  *   block:            16, 32, 64 or 128;  head_dim: 64 or 128;  n_cap < 2^31
- * All buffers are the caller's; nothing needs to be initialised before the first write of
+ * All buffers are the caller's, k and v (and their scales) different ones; nothing needs to be initialised before the first write of
  * a sequence at position 0 (or at any multiple of block). */
 typedef enum { ESA_Q8_E4M3 = 0, ESA_Q8_INT8 = 1 } esa_q8_format_t;
 
@@ -462,13 +462,15 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  *   lse:        NULL or [batch, lq, hq] fp32
  * Scales may be any positive numbers below 2^121, and the codes of attended keys any but
  * e4m3's NaN (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a
- * row of NaN. hq is a multiple of hkv; no limit on
- * their ratio. Codes are exact in the products; softmax weights keep 11 bits or more (22
- * for fp32), and 2^-26 of the largest at least. A large chunk (bf16, head_dim 128, hq / hkv in {1, 2, 4, 8}) dequantises its
- * keys and values into the workspace as bf16 (exact for scales that are powers of two) and
- * rounds its weights to bf16. The workspace is for that alone: ask
- * esa_sparse_attn_q8_workspace_size (256-byte aligned; 0 bytes for other calls). Other
- * errors as for esa_sparse_attn. */
+ * row of NaN. hq is a multiple of hkv; no limit on their ratio. Entries of idx may repeat
+ * (count may be up to topk whatever the length of the middle); entries outside the cache are
+ * clamped into it. Codes are exact in the products; softmax weights keep 11 bits or more (22
+ * for fp32), and 2^-26 of the largest at least. A large chunk (bf16, head_dim 128, hq / hkv
+ * in {1, 2, 4, 8}) dequantises its keys and values into the workspace as bf16 (exact for
+ * scales that are powers of two) and rounds its weights to bf16. The workspace is for that
+ * alone: ask esa_sparse_attn_q8_workspace_size (256-byte aligned; 0 bytes for other calls).
+ * ESA_ERR_UNSUPPORTED for more than 65535 row tiles (hkv * ceil(lq * hq / hkv / 16), / 8 with
+ * up to 8 rows; 24 for bf16 with head_dim 128). Other errors as for esa_sparse_attn. */
 esa_status_t esa_sparse_attn_q8(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, int32_t lq, int64_t c0,
                                 int32_t hq, const int32_t* idx, const int32_t* count, int32_t lists,
                                 esa_params_t p, float scale, void* o, float* lse, void* workspace,
@@ -542,7 +544,8 @@ const char* esa_last_error(void);
  * device. Returns ESA_OK, ESA_ERR_TIMEOUT if a kernel's bounded wait ran out since the
  * last read (the message names the kernel and the wait), ESA_ERR_CUDA if a kernel
  * stopped early on a launch-environment check (e.g. misaligned shared memory), or
- * ESA_ERR_INVALID_ARG if a variable-length call read a length outside [1, n_cap]. */
+ * ESA_ERR_INVALID_ARG if a variable-length call read a length outside [1, n_cap] or a
+ * write to an 8-bit cache read a NaN or an infinity. */
 esa_status_t esa_device_status(void* stream);
 
 /* esa_wait_selftest - runs the bounded-wait path on demand: one CTA waits on a barrier

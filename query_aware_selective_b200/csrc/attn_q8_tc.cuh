@@ -21,10 +21,20 @@
 // weight's value is next to zero), and nothing in TMEM is ever rescaled.
 //
 // Roles: one to three softmax warpgroups (thread = key for S and W, thread = dim for O; up to
-// 8 query rows each, and with few rows two that take turns at the key tiles), one warp that issues the MMAs, two that copy keys, values and
-// scales (16-byte cp.async, 8 lanes a row, into 128-byte-swizzled tiles). TMEM: four
-// buffers of S (two where N leaves no room), two of O. A CTA takes a share of one (sequence, KV head)'s key list; at the end each
-// CTA of a cluster sends every other its part of their dims and merges its own.
+// 8 query rows each, and with few rows two that take turns at the key tiles), one warp that
+// issues the MMAs, two that copy keys, values and scales (16-byte cp.async, 8 lanes a row,
+// into 128-byte-swizzled tiles). TMEM: four buffers of S (two where N leaves no room), two of
+// O. A CTA takes a share of one (sequence, KV head)'s key list; at the end each CTA of a
+// cluster sends every other its part of their dims and merges its own.
+//
+// Bound by HBM with up to 8 rows: 16 sequences x 6.3K keys x 8 heads (206 MB, a CTA per
+// sequence and head) take 38.6 us, 5.3 TB/s; the loop alone streams at 6.4 TB/s, 2.7 us go
+// to the launch, the queries and the first keys, 1.8 us to the last tile and the merge, and
+// 128 units leave 20 of 148 SMs idle. One CTA of six stages an SM beat two of three, 39.7
+// against 42 us. With more rows bound by the softmax warps' issue slots: 20 rows x 24 units
+// (39 MB) take 23 us, a tile of 128 keys 2650 cycles. (Converted to f16 for mma.sync, as
+// attn_q8.cuh does, the same keys took 70 and 77 us: the conversions cost more issue slots
+// than the softmax.)
 #pragma once
 #include "attn_q8.cuh"
 #include "common.cuh"

@@ -228,9 +228,16 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
   }
   const float s = fmaxf(q8_scale_of<FMT>(mx), old);
   const float inv = 1.f / s;                       // exact: powers of two
+  float up = inv;
   if (!finite) {
-    const uint32_t top = __float_as_uint((FMT == kQ8E4M3 ? 448.f : 127.f) * s);
-    each([&](uint32_t v) { return (v & 0x7fffffffu) == 0x7f800000u ? (v & 0x80000000u) | top : v; });
+    // all elements times 2^-10, so that an infinity's stand-in qmax s is finite under every s
+    // (what becomes subnormal is a code of 0 either way)
+    uint32_t top = __float_as_uint((FMT == kQ8E4M3 ? 448.f : 127.f) * 0x1p-10f * s);
+    if constexpr (sizeof(T) == 2) top = (top + 0xffffu) & 0xffff0000u;
+    each([&](uint32_t v) {
+      return (v & 0x7fffffffu) == 0x7f800000u ? (v & 0x80000000u) | top : __float_as_uint(__uint_as_float(v) * 0x1p-10f);
+    });
+    up = inv * 0x1p10f;
   }
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
@@ -244,7 +251,7 @@ __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArg
         if constexpr (sizeof(T) == 4) f[e] = __uint_as_float(x[p][4 * q + e]);
         else f[e] = __uint_as_float((e & 1) ? x[p][2 * q + e / 2] & 0xffff0000u : x[p][2 * q + e / 2] << 16);
       }
-      c[q] = q8_narrow4<FMT>(f, inv);
+      c[q] = q8_narrow4<FMT>(f, up);
     }
     *reinterpret_cast<uint4*>(codes + (base + row0 + p * rpp) * cs + piece * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const Cache
 
 // The whole key list of a chunk (initial, selected, local and the chunk itself; one list
 // per sequence, or one per KV head) as bf16 rows [B, t_pad, Hkv, 128] for the tensor-core
-// attention; rows behind the list are zeros, up to t_pad (a multiple of the key tile).
+// attention; rows behind the list are zeros, to the end of its last key tile.
 // grid as above.
 struct CacheStageArgs {
   const uint8_t* codes[2];
@@ -402,6 +409,7 @@ struct CacheStageArgs {
   int64_t n_cap, nblk, c0, t_pad;
   int lq, hkv, lists, bshift;
 };
+constexpr int kStageTile = 128;           // keys of a tile of the attention; t_pad is a multiple
 
 template <int FMT>
 __global__ void __launch_bounds__(kReadThreads) cache_stage_q8_kernel(const CacheStageArgs a) {
@@ -424,7 +432,8 @@ __global__ void __launch_bounds__(kReadThreads) cache_stage_q8_kernel(const Cach
   }
   q8_move<__nv_bfloat16, FMT>(a.codes[op] + (int64_t)b * a.n_cap * row_bytes + col * 16,
                               a.scale[op] + (int64_t)b * a.nblk * a.hkv + g, row_bytes, a.hkv, a.bshift, pos,
-                              a.out[op] + (int64_t)b * a.t_pad * row_bytes + col * 16, row0, tile.rows, a.t_pad);
+                              a.out[op] + (int64_t)b * a.t_pad * row_bytes + col * 16, row0, tile.rows,
+                              (n_keys + kStageTile - 1) / kStageTile * kStageTile);
 }
 
 }  // namespace esa

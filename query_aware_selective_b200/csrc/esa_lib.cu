@@ -1238,6 +1238,8 @@ esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int6
     return fail(ESA_ERR_INVALID_ARG, "rows of k and v need 16-byte alignment");
   if ((rows > 1 && (krs < width || vrs < width)) || (c.batch > 1 && (kbs < 0 || vbs < 0)))
     return fail(ESA_ERR_INVALID_ARG, "row strides must be >= hkv * head_dim, batch strides >= 0");
+  if (c.k == c.v || c.k_scale == c.v_scale)
+    return fail(ESA_ERR_INVALID_ARG, "keys and values of the cache share a buffer");
   esa::CacheWriteArgs a{};
   a.x[0] = k;
   a.x[1] = v;
@@ -1294,8 +1296,9 @@ bool q8_chunk_form(int64_t batch, int32_t lq, int32_t hq, int32_t hkv, int32_t h
 }
 
 int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
-  const Regions r = regions(c0, p);
-  return cdiv(r.ni + std::min<int64_t>(p.topk, r.n_mid) + (c0 - r.lo) + lq, esa::kTcKeys) * esa::kTcKeys;
+  static_assert(esa::kStageTile == esa::kTcKeys, "staged rows end with a key tile");
+  const Regions r = regions(c0, p);         // a list may name a token twice: up to topk entries
+  return cdiv(r.ni + p.topk + (c0 - r.lo) + lq, esa::kTcKeys) * esa::kTcKeys;
 }
 
 // The largest cluster of up to 8 CTAs (and up to `most`) with which `units` units of work, a

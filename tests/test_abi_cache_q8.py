@@ -68,6 +68,10 @@ def test_write_refusals(lib):
     assert w(kr=512) == INVALID and w(vr=0) == INVALID                        # rows would overlap
     assert w(kb=-8192) == INVALID
     assert w(rows=0, k=None) == _abi.ESA_OK                                   # nothing to write
+    for shared in (dict(vs=2 * FAKE), dict(v=2 * FAKE)):                      # one buffer for keys and values
+        c = cache(**shared)
+        assert lib.esa_cache_write_q8(FAKE, FAKE, 1, 8, 8192, 1024, 8192, 1024, c, 0, None) == INVALID
+        assert b"share a buffer" in lib.esa_last_error()
     f = lib.esa_cache_write_q8_varlen
     assert f(FAKE, FAKE, 1, 1, 1024, 1024, 1024, 1024, cache(), None, None, None) == INVALID
     assert lib.esa_launch_count() == before
@@ -120,7 +124,7 @@ def test_workspace_is_for_chunks_only(lib):
     assert size(1, 512, 32000, 32, 8, 64, 1, p) == 0                          # head_dim 64
     rows = 128 + 2048 + 4096 + 512                                            # 6784 = 53 * 128
     assert size(1, 512, 32000, 32, 8, 128, 1, p) == 2 * rows * 8 * 128 * 2
-    assert size(1, 512, 0, 32, 8, 128, 1, p) == 2 * 512 * 8 * 128 * 2
+    assert size(1, 512, 0, 32, 8, 128, 1, p) == 2 * (2048 + 512) * 8 * 128 * 2   # a list may repeat tokens
     assert size(0, 512, 0, 32, 8, 128, 1, p) == 0
 
 

@@ -232,6 +232,29 @@ def test_write_of_nan_and_infinity(fmt, dtype):
     assert (_numbers(cache.k)[0, :16] == top).all() and (cache.k_scale[0, 0].cpu() == 2.0 ** -100).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_write_of_infinity_beside_the_largest_numbers(fmt, dtype):
+    """qmax times the scale of the type's largest number is past fp32."""
+    big = torch.finfo(dtype).max
+    x = torch.zeros((1, 16, 1, 64), dtype=dtype)
+    x[0, 0, 0, :4] = torch.tensor([big, -big, float("inf"), float("-inf")])
+    cache, clean = _cache(1, 16, 1, 64, fmt, 16), _cache(1, 16, 1, 64, fmt, 16)
+    qas.cache_write_q8(cache, x.to(DEV), x.to(DEV), 0)
+    with pytest.raises(qas.EsaError, match="NaN or infinite"):
+        qas.device_status()
+    y = x.nan_to_num(0.0, 0.0, 0.0)
+    qas.cache_write_q8(clean, y.to(DEV), y.to(DEV), 0)
+    qas.device_status()
+    top = 448.0 if fmt == "e4m3" else 127.0
+    assert torch.equal(cache.k_scale, clean.k_scale) and torch.equal(cache.v_scale, clean.v_scale)
+    for got, want in ((cache.k, clean.k), (cache.v, clean.v)):
+        got, want = _numbers(got), _numbers(want)
+        assert got[0, 0, 0, 2] == top and got[0, 0, 0, 3] == -top
+        want[0, 0, 0, 2:4] = top, -top
+        assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("b,n_cap,hkv,d,block", [(2, 203, 3, 64, 16), (1, 130, 8, 128, 64), (3, 77, 1, 128, 32),
@@ -540,6 +563,24 @@ def test_attention_index_list_outside_the_cache_is_clamped():
         o, lse = qas.sparse_attn_q8(q.to(DEV), cache, n_cap - 1, idx.to(DEV), cnt.to(DEV), p, want_lse=True)
         used = torch.tensor([[min(max(count, 0), 4)]], dtype=torch.int32)
         _check(o, lse, _reference(q, kv, vv, [n_cap - 1], as_read, used, 8, 64), torch.bfloat16, d)
+
+
+@pytest.mark.parametrize("lq,hq,d", [(1, 8, 128), (2, 8, 64), (100, 8, 128), (230, 8, 128)])
+def test_attention_list_longer_than_the_middle(lq, hq, d):
+    """Entries that repeat: a list may hold up to topk of them however short the middle is (a
+    second sequence follows the first one's, so that rows in its place would show)."""
+    b, hkv, n_init, window, topk = 2, 2, 8, 32, 700
+    c0 = 64
+    cache, kv, vv = _filled(b, c0 + lq + 5, hkv, d, "e4m3", 16, [c0 + lq] * b, 651)
+    q = _rand((b, lq, hq, d), 661, torch.bfloat16)
+    gen = torch.Generator().manual_seed(671)
+    idx = torch.randint(n_init, c0 - window, (b, 1, topk), generator=gen, dtype=torch.int32).sort(dim=2).values
+    cnt = torch.tensor([[topk], [topk - 3]], dtype=torch.int32)
+    p = qas.params(n_init, window, topk, 0)
+    chunk = qas._abi.sparse_attn_q8_workspace_size(b, lq, c0, hq, hkv, d, 1, p) > 0
+    assert chunk == (lq == 230)
+    o, lse = qas.sparse_attn_q8(q.to(DEV), cache, c0, idx.to(DEV), cnt.to(DEV), p, want_lse=True)
+    _check(o, lse, _reference(q, kv, vv, [c0] * b, idx, cnt, n_init, window), torch.bfloat16, d, chunk=chunk)
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
