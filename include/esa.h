@@ -460,14 +460,14 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  *   q, o:       [batch, lq, hq, head_dim] of dtype dt (ESA_F32 or ESA_BF16)
  *   idx, count: [batch, lists, p.topk] and [batch, lists] int32, as the selections write them
  *   lse:        NULL or [batch, lq, hq] fp32
- * Scales may be any positive numbers below 2^121, and the codes of attended keys any but
- * e4m3's NaN (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a
+ * Scales of keys may be any positive numbers below 2^121, those of values below 2^98 (under
+ * 2^-100, or zero, they count as 2^-100), and the codes of attended keys any but e4m3's NaN (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a
  * row of NaN. hq is a multiple of hkv; no limit on their ratio. Entries of idx may repeat
  * (count may be up to topk whatever the length of the middle); entries outside the cache are
  * clamped into it. Codes are exact in the products; softmax weights keep 11 bits or more (22
- * for fp32), and 2^-26 of the largest at least. A large chunk (bf16, head_dim 128, hq / hkv
- * in {1, 2, 4, 8}) dequantises its keys and values into the workspace as bf16 (exact for
- * scales that are powers of two) and rounds its weights to bf16. The workspace is for that
+ * for fp32), and 2^-26 of the largest at least. A large chunk of bf16
+ * queries dequantises its keys and values into the workspace as bf16 (exact for scales that
+ * are powers of two) and rounds its weights to bf16. The workspace is for that
  * alone: ask esa_sparse_attn_q8_workspace_size (256-byte aligned; 0 bytes for other calls).
  * ESA_ERR_UNSUPPORTED for more than 65535 row tiles (hkv * ceil(lq * hq / hkv / 16), / 8 with
  * up to 8 rows; 24 for bf16 with head_dim 128). Other errors as for esa_sparse_attn. */

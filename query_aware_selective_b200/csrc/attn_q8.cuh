@@ -157,8 +157,9 @@ __device__ __forceinline__ void q8_transpose(uint32_t wa, uint32_t wb, uint32_t*
 }
 
 // log2 of a value block's scale (within 2^-23 at powers of two; the weights' reciprocal
-// factors are taken from it). Scales under 2^-120, zero among them, count as 2^-120.
-__device__ __forceinline__ float q8_scale_log2(float s) { return __log2f(s < 0x1p-120f ? 0x1p-120f : s); }
+// factors are taken from it). Scales under the least that is written, zero among them, count
+// as that: 2^100 times 2^27 tokens still fit a row sum.
+__device__ __forceinline__ float q8_scale_log2(float s) { return __log2f(s < 0x1p-100f ? 0x1p-100f : s); }
 
 // The exponent of a power of two that brings amax to [2^13, 2^14): queries of any range
 // fit f16, and the elements that matter stay normal there.
@@ -543,15 +544,48 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
   if (csize > 1) cluster_sync_all();                                         // no CTA leaves while it is read
 }
 
-// Chunks: the tensor-core attention over the staged rows [B, t_pad, Hkv, 128] of the whole
-// key list (cache_stage_q8_kernel), so every key tile is one box.
+// Chunks: the tensor-core attention over the staged rows [B, t_pad, Hkv, D] of the whole key
+// list (cache_stage_q8_kernel), so every key tile is one box. Heads of 64 fill the first half
+// of the 128 columns: the maps' rows end there, and a load behind them brings zeros. A group
+// that does not divide 128 rows gathers its queries (heads of 128), or goes in `parts` parts
+// that do, each a head of its own here (heads of 64, whose rows a gather would overrun).
 struct Q8TcProblem : EsaTcProblem {
   int64_t t_pad;
-  __device__ int32_t kv_row(int64_t t) const { return (int32_t)(((int64_t)b * t_pad + t) * hkv + g); }
+  int d;
+  int parts;             // G is that of a part, blockIdx.y counts parts
+  bool boxed;            // Q tiles are boxes
+  __device__ bool setup() {
+    const bool any = EsaTcProblem::setup_at(blockIdx.x);
+    if (lists == 1 || parts == 1 || !any) return any;
+    list = b * lists + g / parts;
+    cnt = min(max(keys.count[list], 0), (int)keys.idx_stride);
+    const int64_t prior = keys.ni + cnt + (c0 - keys.lo);
+    nk += prior - n_prior;
+    n_prior = prior;
+    return true;
+  }
+  __device__ bool q_box(int* y, int* z) const { return boxed && EsaTcProblem::q_box(y, z); }
+  __device__ int32_t kv_row(int64_t t) const { return (int32_t)(((int64_t)b * t_pad + t) * hkv + g / parts); }
   __device__ int kv_box(int j, int* y, int* z) const {
-    *y = g;
+    *y = g / parts;
     *z = (int)((int64_t)b * t_pad + (int64_t)j * kTcKeys);
     return 1;
+  }
+  __device__ void store(int r, int col0, const float* acc, float m2, float l) {
+    if (d == kTcD) return EsaTcProblem::store(r, col0, acc, m2, l);
+    const int R = tile * kTcRows + r;
+    if (R >= lq * G || col0 >= d) return;
+    const int i = R / G, hl = R % G;
+    const int64_t row = ((int64_t)b * lq + i) * hq + g * G + hl;
+    const float inv = 1.f / l;
+    uint4* dst = reinterpret_cast<uint4*>(o + row * d + col0);
+#pragma unroll
+    for (int c = 0; c < kTcD / kTcSplit / 8; ++c)
+      dst[c] = make_uint4(pack_bf16x2(acc[8 * c] * inv, acc[8 * c + 1] * inv),
+                          pack_bf16x2(acc[8 * c + 2] * inv, acc[8 * c + 3] * inv),
+                          pack_bf16x2(acc[8 * c + 4] * inv, acc[8 * c + 5] * inv),
+                          pack_bf16x2(acc[8 * c + 6] * inv, acc[8 * c + 7] * inv));
+    if (lse && col0 == 0) lse[row] = (m2 + __log2f(l)) * 0.69314718055994531f;
   }
 };
 

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const Cache
 }
 
 // The whole key list of a chunk (initial, selected, local and the chunk itself; one list
-// per sequence, or one per KV head) as bf16 rows [B, t_pad, Hkv, 128] for the tensor-core
+// per sequence, or one per KV head) as bf16 rows [B, t_pad, Hkv, D] for the tensor-core
 // attention; rows behind the list are zeros, to the end of its last key tile.
 // grid as above.
 struct CacheStageArgs {
@@ -407,21 +407,21 @@ struct CacheStageArgs {
   __nv_bfloat16* out[2];
   KeyList keys;
   int64_t n_cap, nblk, c0, t_pad;
-  int lq, hkv, lists, bshift;
+  int lq, hkv, d, lists, bshift;
 };
 constexpr int kStageTile = 128;           // keys of a tile of the attention; t_pad is a multiple
 
 template <int FMT>
 __global__ void __launch_bounds__(kReadThreads) cache_stage_q8_kernel(const CacheStageArgs a) {
   const int op = blockIdx.z, b = blockIdx.y;
-  const uint32_t row_bytes = (uint32_t)(a.hkv * 128);
+  const uint32_t row_bytes = (uint32_t)(a.hkv * a.d);
   const ReadTile tile(row_bytes / 16);
   const int rt = blockIdx.x / tile.col_ctas, cc = blockIdx.x - rt * tile.col_ctas;
   const int tr = threadIdx.x / tile.cols, col = cc * kReadThreads + threadIdx.x - tr * tile.cols;
   if (tr >= tile.rows || col * 16 >= row_bytes) return;
   const int64_t row0 = (int64_t)rt * (tile.rows * kReadPer) + tr;
   pdl_wait();
-  const int g = col >> 3, list = a.lists > 1 ? b * a.lists + g : b;
+  const int g = col * 16 / a.d, list = a.lists > 1 ? b * a.lists + g : b;
   const int cnt = min(max(a.keys.count[list], 0), (int)a.keys.idx_stride);
   const int64_t n_keys = a.keys.ni + cnt + (a.c0 - a.keys.lo) + a.lq;
   int pos[kReadPer];

@@ -307,15 +307,15 @@ esa_status_t make_tmap_rows_bf16(CUtensorMap* m, const void* base, uint64_t rows
   return ESA_OK;
 }
 
-// 3D tensor map over bf16 [tokens, heads, 128]; a box is box_tokens consecutive tokens x
+// 3D tensor map over bf16 [tokens, heads, dim]; a box is box_tokens consecutive tokens x
 // box_heads consecutive heads x 64 columns, 128-byte swizzle (rows ordered token-major).
 esa_status_t make_tmap_box_bf16(CUtensorMap* m, const void* base, uint64_t heads, uint64_t tokens,
-                                uint32_t box_heads, uint32_t box_tokens) {
+                                uint32_t box_heads, uint32_t box_tokens, uint64_t dim = 128) {
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   esa_status_t st = get_encoder(&encode);
   if (st != ESA_OK) return st;
-  cuuint64_t dims[3] = {128, heads, tokens};
-  cuuint64_t strides[2] = {128 * 2, heads * 128 * 2};
+  cuuint64_t dims[3] = {dim, heads, tokens};
+  cuuint64_t strides[2] = {dim * 2, heads * dim * 2};
   cuuint32_t box[3] = {64, box_heads, box_tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -1281,18 +1281,26 @@ esa_status_t cache_write_impl(const void* k, const void* v, esa_dtype_t dt, int6
 // Query rows of a KV head in tiles of up to 24 (attn_q8_tc_kernel).
 int64_t q8_row_tiles(int64_t rows) { return cdiv(rows, 24); }
 
+// Heads of a group that 128-row boxes of queries take: the largest power of two in it.
+int q8_box_group(int g) { return std::min(g & -g, esa::kTcRows); }
+
 // Whether a call dequantises its key list for attn_tc_kernel (128 rows a CTA, every CTA the
-// whole list: 62 to 65 us for 6.3K keys whatever the rows, until its CTAs outnumber the SMs)
-// or runs attn_q8_tc_kernel on the codes. The latter splits each list over clusters while
-// its units of work (sequence, KV head, 24 rows) leave SMs free for that: 22 us for 6.3K
-// keys with 24 units, 44 with up to 74, 80 with up to 148, a wave more for each further
-// 148. So: codes up to half the SMs' number of units (and under 64 rows, whose 128-row
-// tiles would be half empty), the tensor-core chunk above.
+// whole list: 60 to 65 us for 6.3K keys whatever the rows, until its CTAs outnumber the SMs,
+// and 0.8 us of staging for every sequence and KV head of 128) or runs on the codes.
+// Heads of 128: attn_q8_tc_kernel splits each list over clusters while its units of work
+// (sequence, KV head, 24 rows) leave SMs free for that: 22 us for 24 units, 44 with up to 74,
+// 75 to 80 with up to 148, a wave more for each further 148; with 8 heads on 40 and one
+// sequence, 130 rows (48 units) 42 us against 67 staged, 255 rows (88) 75 against 67, 2560
+// rows 451 against 132. So: codes up to half the SMs' number of units, and under 64 rows,
+// whose 128-row tiles would be half empty. Heads of 64: attn_q8_kernel takes 16 rows a unit,
+// 62 us for 224 units against 70 staged, 92 for 416 against 71, 220 for 1024 against 68, and
+// with 128 (sequence, KV head)s 69 us for 20 rows against 109, 133 for 52 against 109.
 bool q8_chunk_form(int64_t batch, int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
   const int g = hq / hkv;
-  const int64_t rows = (int64_t)lq * g;
-  return dt == ESA_BF16 && head_dim == 128 && rows >= 64 && (g == 1 || g == 2 || g == 4 || g == 8) &&
-         batch * hkv * q8_row_tiles(rows) > 74;
+  const int64_t rows = (int64_t)lq * g, n = batch * hkv;
+  if (dt != ESA_BF16) return false;
+  if (head_dim == 128) return rows >= 64 && n * q8_row_tiles(rows) > 74;
+  return (int64_t)lq * q8_box_group(g) > 32 && n * cdiv(rows, 16) > 296;
 }
 
 int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
@@ -1388,8 +1396,11 @@ esa_status_t dispatch_attn_q8_tc(const esa::AttnQ8Args& a, int32_t batch, int64_
 esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, int64_t c0, int32_t hq,
                            const esa::KeyList& keys, int lists, const esa_params_t& p, float sl2, void* o, float* lse,
                            void* workspace, cudaStream_t s) {
-  const int g = hq / c.hkv;
+  const int group = hq / c.hkv, box = q8_box_group(group);
+  const bool boxed = box == group || c.head_dim == 64;
+  const int g = boxed ? box : group, parts = group / g;
   const int64_t t_pad = q8_staged_rows(lq, c0, p);
+  if ((int64_t)c.hkv * parts > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 parts of groups");
   if (c.batch * t_pad * c.hkv >= ((int64_t)1 << 31) || (int64_t)c.batch * lq * hq >= ((int64_t)1 << 31))
     return fail(ESA_ERR_UNSUPPORTED, "more than 2^31 K/V or Q rows");
   static const char what = 0;
@@ -1399,9 +1410,12 @@ esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, i
   uint8_t* ks = static_cast<uint8_t*>(workspace);
   uint8_t* vs = ks + up256((size_t)c.batch * t_pad * c.hkv * c.head_dim * 2);
   CUtensorMap bq, bk, bv;
-  if ((st = make_tmap_box_bf16(&bq, q, hq, (uint64_t)c.batch * lq, g, esa::kTcRows / g)) != ESA_OK) return st;
-  if ((st = make_tmap_box_bf16(&bk, ks, c.hkv, (uint64_t)c.batch * t_pad, 1, esa::kTcKeys)) != ESA_OK) return st;
-  if ((st = make_tmap_box_bf16(&bv, vs, c.hkv, (uint64_t)c.batch * t_pad, 1, esa::kTcKeys)) != ESA_OK) return st;
+  st = boxed ? make_tmap_box_bf16(&bq, q, hq, (uint64_t)c.batch * lq, g, esa::kTcRows / g, c.head_dim)
+             : make_tmap_rows_bf16(&bq, q, (uint64_t)c.batch * lq * hq);
+  if (st != ESA_OK) return st;
+  const uint64_t staged = (uint64_t)c.batch * t_pad;
+  if ((st = make_tmap_box_bf16(&bk, ks, c.hkv, staged, 1, esa::kTcKeys, c.head_dim)) != ESA_OK) return st;
+  if ((st = make_tmap_box_bf16(&bv, vs, c.hkv, staged, 1, esa::kTcKeys, c.head_dim)) != ESA_OK) return st;
   esa::CacheStageArgs a{};
   a.codes[0] = static_cast<const uint8_t*>(c.k);
   a.codes[1] = static_cast<const uint8_t*>(c.v);
@@ -1416,9 +1430,10 @@ esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, i
   a.t_pad = t_pad;
   a.lq = lq;
   a.hkv = c.hkv;
+  a.d = c.head_dim;
   a.lists = lists;
   a.bshift = log2_of(c.block);
-  const esa::ReadTile tile(c.hkv * 8);
+  const esa::ReadTile tile(c.hkv * c.head_dim / 16);
   const dim3 sgrid((unsigned)(cdiv(t_pad, tile.rows * esa::kReadPer) * tile.col_ctas), c.batch, 2);
   st = launch_q8(c.format == ESA_Q8_E4M3 ? esa::cache_stage_q8_kernel<esa::kQ8E4M3>
                                          : esa::cache_stage_q8_kernel<esa::kQ8Int8>,
@@ -1438,8 +1453,12 @@ esa_status_t attn_q8_chunk(const void* q, const esa_cache_q8_t& c, int32_t lq, i
   pr.sl2 = sl2;
   pr.lists = lists;
   pr.t_pad = t_pad;
-  const dim3 grid((unsigned)cdiv((int64_t)lq * g, esa::kTcRows), c.hkv, c.batch);
-  // every tile is a box, so the row-gather maps are never read: the box maps stand in
+  pr.d = c.head_dim;
+  pr.parts = parts;
+  pr.boxed = boxed;
+  const dim3 grid((unsigned)cdiv((int64_t)lq * g, esa::kTcRows), c.hkv * parts, c.batch);
+  // every key tile is a box: the box maps stand in for the gather maps; bq is the one of the
+  // two forms of query tile that there is
   esa::attn_tc_kernel<esa::Q8TcProblem><<<grid, esa::kTcThreads, esa::kTcSmemBytes, s>>>(bq, bk, bv, bq, bk, bv, bk,
                                                                                         bv, pr);
   ESA_LAUNCH_CHECK("attn_tc_kernel<q8>");

@@ -107,7 +107,7 @@ def test_attention_refusals(lib):
     assert a(p=_abi.params(128, 512, 0, 2)) == INVALID and a(p=_abi.params(-1, 512, 4, 2)) == INVALID
     assert a(p=_abi.params(128, 512, 2 ** 31 - 1, 2)) == UNSUPPORTED
     assert a(lq=64, ws=None) == WORKSPACE and a(lq=64, nb=1024) == WORKSPACE and a(lq=64, ws=FAKE + 64) == WORKSPACE
-    assert a(lq=4000, c0=0, hq=8 * 300, n_cap=4096, d=64) == UNSUPPORTED     # 75000 row tiles of 16
+    assert a(dt=0, lq=4000, c0=0, hq=8 * 300, n_cap=4096, d=64) == UNSUPPORTED   # 75000 row tiles of 16
     f = lib.esa_sparse_attn_q8_varlen
     assert f(FAKE, 1, cache(), None, 32, FAKE, FAKE, 1, good, 0.0, FAKE, None, None) == INVALID
     assert f(FAKE, 1, cache(), FAKE, 32, FAKE, FAKE, 3, good, 0.0, FAKE, None, None) == INVALID
@@ -119,11 +119,15 @@ def test_workspace_is_for_chunks_only(lib):
     size = _abi.sparse_attn_q8_workspace_size
     assert size(16, 1, 131071, 32, 8, 128, 1, p) == 0                         # decode
     assert size(1, 15, 32000, 32, 8, 128, 1, p) == 0                          # 60 rows
-    assert size(1, 64, 32000, 40, 8, 128, 1, p) == 0                          # groups of 5
+    assert size(1, 3, 32000, 256, 8, 128, 1, p) == 0                          # 96 rows of 8 heads: 32 units
     assert size(1, 512, 32000, 32, 8, 128, 0, p) == 0                         # fp32
-    assert size(1, 512, 32000, 32, 8, 64, 1, p) == 0                          # head_dim 64
+    assert size(1, 16, 32000, 32, 8, 64, 1, p) == 0                           # head_dim 64: 64 rows, 32 units
+    assert size(16, 16, 32000, 40, 8, 64, 1, p) == 0                          # a fifth of the heads at a time: 16 rows
     rows = 128 + 2048 + 4096 + 512                                            # 6784 = 53 * 128
     assert size(1, 512, 32000, 32, 8, 128, 1, p) == 2 * rows * 8 * 128 * 2
+    assert size(1, 512, 32000, 40, 8, 128, 1, p) == 2 * rows * 8 * 128 * 2     # groups of 5
+    assert size(1, 512, 32000, 32, 8, 64, 1, p) == 2 * rows * 8 * 64 * 2
+    assert size(1, 512, 32000, 40, 8, 64, 1, p) == 2 * rows * 8 * 64 * 2
     assert size(1, 512, 0, 32, 8, 128, 1, p) == 2 * (2048 + 512) * 8 * 128 * 2   # a list may repeat tokens
     assert size(0, 512, 0, 32, 8, 128, 1, p) == 0
 

@@ -433,6 +433,55 @@ def test_attention_chunk(fmt, chunk, b, lq, n_cap, hq, hkv, block, lists, n_init
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("chunk,b,lq,n_cap,hq,hkv,d,block,lists,n_init,window,topk", [
+    (True, 2, 210, 1100, 10, 2, 128, 32, 2, 16, 200, 150),       # G 5, gathered queries, a list per head, ragged
+    (True, 1, 65, 1000, 56, 2, 128, 64, 1, 0, 130, 64),          # G 28
+    (True, 3, 9, 700, 144, 2, 128, 16, 2, 32, 64, 40),           # G 72, tiles that end inside a query's heads
+    (True, 1, 160, 1500, 32, 8, 64, 64, 1, 32, 256, 300),        # heads of 64: G 4
+    (True, 2, 301, 1200, 8, 8, 64, 16, 8, 16, 200, 150),         # G 1, a list per head
+    (True, 2, 90, 900, 28, 4, 64, 128, 4, 128, 100, 90),         # G 7: a head at a time, a list per KV head
+    (True, 1, 400, 400, 24, 2, 64, 32, 1, 16, 64, 32),           # G 12: four heads at a time, the first chunk
+    (True, 3, 33, 555, 160, 2, 64, 64, 2, 8, 31, 77),            # G 80: sixteen at a time
+    (False, 2, 20, 800, 28, 4, 64, 128, 4, 128, 100, 90),        # the same shapes, too few rows of a head
+])
+def test_attention_chunk_any_group_and_heads_of_64(fmt, chunk, b, lq, n_cap, hq, hkv, d, block, lists, n_init, window,
+                                                   topk):
+    c0 = max(0, n_cap - lq - 3)
+    cache, kv, vv = _filled(b, n_cap, hkv, d, fmt, block, [c0 + lq] * b, 133)
+    q = _rand((b, lq, hq, d), 143, torch.bfloat16)
+    idx, cnt = _lists([c0] * b, lists, n_init, window, topk, 153)
+    p = qas.params(n_init, window, topk, 2, 10.0)
+    assert (qas._abi.sparse_attn_q8_workspace_size(b, lq, c0, hq, hkv, d, 1, p) > 0) == chunk
+    guard = torch.full((b * lq * hq * d + 256,), 7.0, dtype=torch.bfloat16, device=DEV)
+    o, lse = qas.sparse_attn_q8(q.to(DEV), cache, c0, idx.to(DEV), cnt.to(DEV), p, want_lse=True,
+                                out=guard[128:-128].view(b, lq, hq, d))
+    _check(o, lse, _reference(q, kv, vv, [c0] * b, idx, cnt, n_init, window), torch.bfloat16, d, chunk=chunk)
+    assert (guard[:128] == 7).all() and (guard[-128:] == 7).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,lq", [(10, 2, 128, 210), (28, 4, 64, 140)])
+def test_attention_chunk_nan_and_infinity_stay_in_their_rows(hq, hkv, d, lq):
+    """A query row with a NaN or an infinity, beside rows of another head and of another query."""
+    n_cap = 600
+    c0 = n_cap - lq
+    cache, kv, vv = _filled(2, n_cap, hkv, d, "e4m3", 32, [n_cap] * 2, 135)
+    q = _rand((2, lq, hq, d), 145, torch.bfloat16)
+    bad = q.clone()
+    bad[0, 3, 1, d - 1], bad[0, 7, 0, 0], bad[1, lq - 1, hq - 1, 5] = float("nan"), float("inf"), float("-inf")
+    idx, cnt = _lists([c0] * 2, 1, 8, 64, 50, 155)
+    p = qas.params(8, 64, 50, 0)
+    assert qas._abi.sparse_attn_q8_workspace_size(2, lq, c0, hq, hkv, d, 1, p) > 0
+    a = (c0, idx.to(DEV), cnt.to(DEV), p)
+    clean, _ = qas.sparse_attn_q8(q.to(DEV), cache, *a)
+    got, _ = qas.sparse_attn_q8(bad.to(DEV), cache, *a)
+    qas.device_status()
+    hit = torch.zeros((2, lq, hq), dtype=torch.bool)
+    hit[0, 3, 1] = hit[0, 7, 0] = hit[1, lq - 1, hq - 1] = True
+    assert got.cpu()[hit].isnan().all()
+    assert torch.equal(got.cpu()[~hit], clean.cpu()[~hit])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("lists", [1, 2])
 @pytest.mark.parametrize("dtype,hq,d", [(torch.bfloat16, 8, 128), (torch.float32, 6, 64)])
 def test_attention_varlen(fmt, lists, dtype, hq, d):
