@@ -555,13 +555,14 @@ struct Q8TcProblem : EsaTcProblem {
   int parts;             // G is that of a part, blockIdx.y counts parts
   bool boxed;            // Q tiles are boxes
   __device__ bool setup() {
-    const bool any = EsaTcProblem::setup_at(blockIdx.x);
-    if (lists == 1 || parts == 1 || !any) return any;
-    list = b * lists + g / parts;
+    tile = blockIdx.x;
+    g = blockIdx.y;
+    b = blockIdx.z;
+    if (tile * kTcRows >= lq * G) return false;
+    list = lists > 1 ? b * lists + g / parts : b;              // the list of the part's KV head
     cnt = min(max(keys.count[list], 0), (int)keys.idx_stride);
-    const int64_t prior = keys.ni + cnt + (c0 - keys.lo);
-    nk += prior - n_prior;
-    n_prior = prior;
+    n_prior = keys.ni + cnt + (c0 - keys.lo);
+    nk = n_prior + min(lq - 1, (tile * kTcRows + kTcRows - 1) / G) + 1;
     return true;
   }
   __device__ bool q_box(int* y, int* z) const { return boxed && EsaTcProblem::q_box(y, z); }
