@@ -143,7 +143,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&v)[NC]) {
 __device__ __forceinline__ void st_dsmem_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// a row's value from its pieces (v[p * WR + r])
+// A row's value from its pieces (v[p * WR + r]): in units of piece 0, or of piece 1 for four
+// digits. Digits are joined in pairs as integers (sums of 128 products: 2^21, 2^28 joined).
 template <int FMT, int WR, int NP>
 __device__ __forceinline__ float q8_join(const uint32_t* v, int r) {
   if constexpr (FMT == kQ8E4M3) {
@@ -152,10 +153,10 @@ __device__ __forceinline__ float q8_join(const uint32_t* v, int r) {
     for (int p = NP - 2; p >= 0; --p) x = fmaf(x, 0.0625f, __uint_as_float(v[p * WR + r]));
     return x;
   } else {
-    float x = (float)(int)v[(NP - 1) * WR + r];
-#pragma unroll
-    for (int p = NP - 2; p >= 0; --p) x = fmaf(x, 0.0078125f, (float)(int)v[p * WR + r]);
-    return x;
+    static_assert(NP == 3 || NP == 4);
+    const int lo = (int)v[(NP - 2) * WR + r] * 128 + (int)v[(NP - 1) * WR + r];
+    const int hi = NP == 3 ? (int)v[r] : (int)v[r] * 128 + (int)v[WR + r];
+    return fmaf((float)lo, 0x1p-14f, (float)hi);
   }
 }
 // Two values as pieces: byte 0 of pc[p] is piece p of x0, byte 1 of x1. e4m3: |x| <= 448;
@@ -184,6 +185,34 @@ __device__ __forceinline__ void q8_split2(float x0, float x1, uint32_t* pc) {
     }
   }
 }
+// Four weights >= 0 (a row each) as pieces: byte r of pc[p] is piece p of x[r].
+template <int FMT, int NP>
+__device__ __forceinline__ void q8_split4(const float* x, uint32_t* pc) {
+  if constexpr (FMT == kQ8E4M3) {
+    uint32_t lo[NP], hi[NP];
+    q8_split2<FMT, NP>(x[0], x[1], lo);
+    q8_split2<FMT, NP>(x[2], x[3], hi);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) pc[p] = __byte_perm(lo[p], hi[p], 0x5410);
+  } else {
+    // 28 bits spread to four bytes of 7: the halves first, then the digits of both (sums of
+    // bits that do not meet), and the 4 x 4 bytes transposed
+    static_assert(NP == 4);
+    uint32_t y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t i = (uint32_t)__float2int_rn(x[r]);
+      const uint32_t t = (i & 0x0fffc000u) * 3u + i;
+      y[r] = t + (t & 0x3f803f80u);
+    }
+    const uint32_t a = __byte_perm(y[0], y[1], 0x5140), b = __byte_perm(y[2], y[3], 0x5140);
+    const uint32_t c = __byte_perm(y[0], y[1], 0x7362), d = __byte_perm(y[2], y[3], 0x7362);
+    pc[0] = __byte_perm(c, d, 0x7632);
+    pc[1] = __byte_perm(c, d, 0x5410);
+    pc[2] = __byte_perm(a, b, 0x7632);
+    pc[3] = __byte_perm(a, b, 0x5410);
+  }
+}
 
 // Dims that each CTA of a cluster merges, a multiple of 4 (the last CTA the rest, if any).
 __device__ __forceinline__ int q8_dims_per(int csize) { return ((128 + csize - 1) / csize + 3) & ~3; }
@@ -197,8 +226,8 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
   constexpr int kBarTmem = RG * TG + 1, kBarQ = RG * TG + 2;      // named barriers (1 .. RG * TG: the warpgroups)
   // a weight of 1 (its tile's largest) goes in as 2^8 (e4m3, <= 448), 2^27 (int8, <= 127 * 2^21)
   constexpr float kTop = FMT == kQ8E4M3 ? 8.f : 27.f;
-  // units of the first piece of a query and of a weight
-  constexpr float kUnitQ = FMT == kQ8E4M3 ? 1.f : 0x1p14f, kUnitW = FMT == kQ8E4M3 ? 1.f : 0x1p21f;
+  // units of q8_join for a query and for a weight
+  constexpr float kUnitQ = FMT == kQ8E4M3 ? 1.f : 0x1p14f, kUnitW = FMT == kQ8E4M3 ? 1.f : 0x1p14f;
   extern __shared__ __align__(1024) uint8_t qtsm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(qtsm);
@@ -515,13 +544,12 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       uint32_t ww[NW + 1][WR / 4];
 #pragma unroll
       for (int r = 0; r < WR; r += 4) {
-        uint32_t lo[NW], hi[NW];
+        uint32_t pc[NW];
 #pragma unroll
         for (int u = 0; u < 4; ++u) x[r + u] = fast_exp2(x[r + u] - (mt[r + u] == -INFINITY ? 0.f : mt[r + u]) + kTop);
-        q8_split2<FMT, NW>(x[r], x[r + 1], lo);
-        q8_split2<FMT, NW>(x[r + 2], x[r + 3], hi);
+        q8_split4<FMT, NW>(x + r, pc);
 #pragma unroll
-        for (int p = 0; p < NW; ++p) ww[p][r / 4] = __byte_perm(lo[p], hi[p], 0x5410);
+        for (int p = 0; p < NW; ++p) ww[p][r / 4] = pc[p];
         ww[NW][r / 4] = 0u;
       }
       const uint32_t wb = base + Sh::kW + (j & 1) * N * 128 + key * 16;
