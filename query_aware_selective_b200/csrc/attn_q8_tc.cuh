@@ -300,11 +300,11 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     tmem = sm.tmem_base;
   }
 
-  float o[WR], m[WR], l[WR];
+  float o[WR], l[WR];
+  float m = -INFINITY;                              // of row lane % WR
 #pragma unroll
   for (int r = 0; r < WR; ++r) {
     o[r] = 0.f;
-    m[r] = -INFINITY;
     l[r] = 0.f;
   }
 
@@ -481,6 +481,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     for (int q = 0; q < WR; ++q) xs[q] = sm_xs[row_wg + q];
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + rg * NW * WR;
     float al[WR], be[WR];                           // the tile's factors on o and on its own O
+    const int row_own = lane % WR;                  // this lane finds them for one row
     auto spin_warp = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, site));
     };
@@ -515,30 +516,26 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
           if (t0 + key >= n_prior + min(r0 + row_wg + r, a.lq * a.G - 1) / a.G + 1) x[r] = -INFINITY;
       }
       // the tile's maximum of each row
-      float mt[WR];
       // [warp][RT]; two buffers in turn: a warp that writes one has passed the barrier of the
       // tile in between, and with it every warp's reads of the maxima before that
-      float4* mx = reinterpret_cast<float4*>(smf + Sh::kMax + (2 * tg + ((j / TG) & 1)) * 4 * RT + row_wg);
+      float* mx = smf + Sh::kMax + (2 * tg + ((j / TG) & 1)) * 4 * RT + row_wg;
+      {
+        float mw[WR];
 #pragma unroll
-      for (int r = 0; r < WR; ++r) mt[r] = redux_max(x[r]);
-      if (lane == 0) {
+        for (int r = 0; r < WR; ++r) mw[r] = redux_max(x[r]);
+        if (lane == 0) {
 #pragma unroll
-        for (int r = 0; r < WR; r += 4)
-          mx[((warp & 3) * RT + r) / 4] = make_float4(mt[r], mt[r + 1], mt[r + 2], mt[r + 3]);
+          for (int r = 0; r < WR; r += 4)
+            *reinterpret_cast<float4*>(mx + (warp & 3) * RT + r) = make_float4(mw[r], mw[r + 1], mw[r + 2], mw[r + 3]);
+        }
       }
       // the O of this warpgroup's tile before (PV_j will overwrite it if TG is 2, and the W
       // buffer below was its own)
       if (j >= TG) ok = ok && drain(j - TG);
       // a named barrier has no time limit: the four warps leave together if a wait ran out
       if (!(ok = bar_all(bar_wg, 128, ok))) break;
-#pragma unroll
-      for (int r = 0; r < WR; r += 4) {
-        const float4 m0 = mx[r / 4], m1 = mx[(RT + r) / 4], m2 = mx[(2 * RT + r) / 4], m3 = mx[(3 * RT + r) / 4];
-        mt[r] = fmaxf(fmaxf(m0.x, m1.x), fmaxf(m2.x, m3.x));
-        mt[r + 1] = fmaxf(fmaxf(m0.y, m1.y), fmaxf(m2.y, m3.y));
-        mt[r + 2] = fmaxf(fmaxf(m0.z, m1.z), fmaxf(m2.z, m3.z));
-        mt[r + 3] = fmaxf(fmaxf(m0.w, m1.w), fmaxf(m2.w, m3.w));
-      }
+      const float mt = fmaxf(fmaxf(mx[row_own], mx[RT + row_own]), fmaxf(mx[2 * RT + row_own], mx[3 * RT + row_own]));
+      const float top = (mt == -INFINITY ? 0.f : mt) - kTop;
       // weights, as pieces, to this key's row of the W buffer: [16 columns][128 keys][16 bytes]
       const float iv = fast_exp2(-lv - kTop);
       uint32_t ww[NW + 1][WR / 4];
@@ -546,7 +543,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       for (int r = 0; r < WR; r += 4) {
         uint32_t pc[NW];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[r + u] = fast_exp2(x[r + u] - (mt[r + u] == -INFINITY ? 0.f : mt[r + u]) + kTop);
+        for (int u = 0; u < 4; ++u) x[r + u] = fast_exp2(x[r + u] - __shfl_sync(0xffffffffu, top, r + u));
         q8_split4<FMT, NW>(x + r, pc);
 #pragma unroll
         for (int p = 0; p < NW; ++p) ww[p][r / 4] = pc[p];
@@ -566,15 +563,14 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive_warp(&sm.w_full[j & 1]);
+      const float mn = fmaxf(m, mt), mr = mn == -INFINITY ? 0.f : mn;
+      const float al_own = fast_exp2(m - mr), be_own = fast_exp2(mt - mr);
+      m = mn;
 #pragma unroll
       for (int r = 0; r < WR; ++r) {
-        const float mn = fmaxf(m[r], mt[r]);
-        const float mr = mn == -INFINITY ? 0.f : mn;
-        al[r] = fast_exp2(m[r] - mr);
-        const float bt = fast_exp2(mt[r] - mr);
-        l[r] = fmaf(l[r], al[r], x[r] * iv * bt);
-        be[r] = bt * kUnitW;
-        m[r] = mn;
+        al[r] = __shfl_sync(0xffffffffu, al_own, r);
+        be[r] = __shfl_sync(0xffffffffu, be_own, r);
+        l[r] = fmaf(l[r], al[r], x[r] * iv * be[r]);
       }
     }
     const int last = (nt - 1 - tg) / TG * TG + tg;  // the warpgroup's last tile, if it had one
@@ -600,10 +596,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       const float* lw = sm_l + tg * 4 * RT + r;
       const float L = (lw[0] + lw[RT]) + (lw[2 * RT] + lw[3 * RT]);
       const uint32_t p = dsmem_map(my_ml, to) + (part * RT + r) * 8;
-      float mm = m[0];
-#pragma unroll
-      for (int q = 1; q < WR; ++q) mm = it % WR == q ? m[q] : mm;
-      st_dsmem_f32(p, mm);
+      st_dsmem_f32(p, m);                           // (it % WR is lane % WR)
       st_dsmem_f32(p + 4, L);
     }
   }
@@ -633,7 +626,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     }
     const int i = a.lq == 1 ? 0 : (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
     const int64_t row = ((int64_t)b * a.lq + i) * a.hq + g * a.G + hl;
-    const float inv = (FMT == kQ8E4M3 ? 0x1p-8f : 0x1p-27f) / L;
+    const float inv = (FMT == kQ8E4M3 ? 0x1p-8f : 0x1p-27f) * kUnitW / L;
     uint2 w;
     w.x = bf16x2_rn(O.x * inv, O.y * inv);
     w.y = bf16x2_rn(O.z * inv, O.w * inv);
