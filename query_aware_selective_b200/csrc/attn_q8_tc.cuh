@@ -529,9 +529,10 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
             *reinterpret_cast<float4*>(mx + (warp & 3) * RT + r) = make_float4(mw[r], mw[r + 1], mw[r + 2], mw[r + 3]);
         }
       }
-      // the O of this warpgroup's tile before (PV_j will overwrite it if TG is 2, and the W
-      // buffer below was its own)
-      if (j >= TG) ok = ok && drain(j - TG);
+      // With two tile groups, now the O of this warpgroup's tile before: PV_j will overwrite it,
+      // and the W buffer below was its own. (With one, both are those of tile j - 2, which was
+      // drained; its O_{j - 1} can wait until W_j is out.)
+      if (TG == 2 && j >= TG) ok = ok && drain(j - TG);
       // a named barrier has no time limit: the four warps leave together if a wait ran out
       if (!(ok = bar_all(bar_wg, 128, ok))) break;
       const float mt = fmaxf(fmaxf(mx[row_own], mx[RT + row_own]), fmaxf(mx[2 * RT + row_own], mx[3 * RT + row_own]));
@@ -563,6 +564,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive_warp(&sm.w_full[j & 1]);
+      if (TG == 1 && j >= TG) ok = ok && drain(j - TG);
       const float mn = fmaxf(m, mt), mr = mn == -INFINITY ? 0.f : mn;
       const float al_own = fast_exp2(m - mr), be_own = fast_exp2(mt - mr);
       m = mn;
