@@ -121,6 +121,20 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t k_bytes
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// Whether both phases have completed, in the time of one test.
+__device__ __forceinline__ bool mbar_test_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -259,6 +273,18 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     for (int u = 0; u < NST; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) raw[u][h] = __ldg(entry(u, prow + 32 * h));
+  }
+  // queries: thread (r, part) of the first tile group takes DPT dims of row r, loaded now for
+  // the time that the list's length and the setup take
+  constexpr int TPR = 128 / WR, DPT = 128 / TPR;
+  const int q_row = (warp >> 2) % RG * WR + (threadIdx.x & 127) / TPR, q_part = (threadIdx.x & 127) % TPR;
+  uint2 q_raw[DPT / 4];
+  if (warp < 4 * RG) {
+    const int rr = min(tile * RT + q_row, a.lq * a.G - 1), i = rr / a.G, hl = rr - i * a.G;
+    const uint2* qp = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) +
+        (((int64_t)b * a.lq + i) * a.hq + g * a.G + hl) * 128 + q_part * DPT);
+#pragma unroll
+    for (int e = 0; e < DPT / 4; ++e) q_raw[e] = __ldg(qp + e);
   }
   const int32_t n_listed = kl.count[list];
   if (threadIdx.x == 0) {
@@ -430,19 +456,16 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     const int key = threadIdx.x & 127;                    // key of a tile, for S and W; the dim, for O
     const uint32_t bar_wg = 1 + (warp >> 2);              // named barrier of the warpgroup
     const int row_wg = rg * WR;                           // its first row of the tile
-    // queries as pieces: thread (r, part) takes DPT dims of row r
-    constexpr int TPR = 128 / WR, DPT = 128 / TPR;
     float xs[WR];                                   // logit factor of each row
     if (tg == 0) {
-      const int r = row_wg + key / TPR, part = key % TPR;
-      const int rr = min(r0 + r, a.lq * a.G - 1), i = rr / a.G, hl = rr - i * a.G;
-      const __nv_bfloat16* qp =
-          static_cast<const __nv_bfloat16*>(a.q) + (((int64_t)b * a.lq + i) * a.hq + g * a.G + hl) * 128 + part * DPT;
+      // queries as pieces
+      const int r = q_row, part = q_part;
       float f[DPT];
       uint32_t mx = 0;                              // largest magnitude, as bits (in the order of the values)
 #pragma unroll
       for (int e = 0; e < DPT; e += 4) {
-        load4(qp + e, f + e);
+        const float2 f01 = bf16x2_to_float2(q_raw[e / 4].x), f23 = bf16x2_to_float2(q_raw[e / 4].y);
+        f[e] = f01.x; f[e + 1] = f01.y; f[e + 2] = f23.x; f[e + 3] = f23.y;
 #pragma unroll
         for (int u = 0; u < 4; ++u) mx = max(mx, __float_as_uint(f[e + u]) & 0x7fffffffu);
       }
@@ -497,7 +520,8 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     bool ok = true;
     for (int j = tg; j < nt; j += TG) {
       // (full: the scales, which this warp reads itself)
-      ok = ok && spin_warp(&sm.s_full[j % NS], (j / NS) & 1, 713) && spin_warp(&sm.full[j % NST], (j / NST) & 1, 715);
+      ok = ok && (__all_sync(0xffffffffu, mbar_test_both(&sm.s_full[j % NS], (j / NS) & 1, &sm.full[j % NST], (j / NST) & 1)) ||
+                  (spin_warp(&sm.s_full[j % NS], (j / NS) & 1, 713) && spin_warp(&sm.full[j % NST], (j / NST) & 1, 715)));
       tc_fence_after();
       float x[WR];
       const float* sc = reinterpret_cast<const float*>(qtsm + (j % NST) * kQtStage + 2 * kQtTile);
@@ -609,16 +633,18 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
   if (warp == kMmaWarp) tmem_dealloc(tmem, Sh::kCols);
   if (csize > 1) cluster_sync_all();                // every CTA's rows are here
   if (*abort_flag) return;
-  const int per = q8_dims_per(csize), d0 = rank * per, d = lane * 4;
-  if (d >= min(per, 128 - d0)) return;
-  for (int r = warp; r < nrow; r += Sh::kThreads / 32) {         // a row per warp, four dims per lane
+  const int per = q8_dims_per(csize), d0 = rank * per, d_items = min(per, 128 - d0) / 4;
+  for (int it = threadIdx.x; it < nrow * d_items; it += Sh::kThreads) {      // four dims of a row
+    const int r = it / d_items, d = (it - r * d_items) * 4;
     const int parts = csize * TG;
     const float* ml = smf + Sh::kMl + r * 2;        // [parts][RT][2]
     const float* po = smf + Sh::kO + r * per * parts + d;
     float M = -INFINITY;
+#pragma unroll 4
     for (int u = 0; u < parts; ++u) M = fmaxf(M, ml[u * RT * 2]);
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int u = 0; u < parts; ++u) {
       const float2 z = *reinterpret_cast<const float2*>(ml + u * RT * 2);
       const float4 x = *reinterpret_cast<const float4*>(po + u * per);
