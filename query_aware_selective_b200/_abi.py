@@ -507,7 +507,7 @@ def cache_q8(batch: int, n_cap: int, hkv: int, head_dim: int, dtype: torch.dtype
 # (The helpers below are written for few interpreter steps: a call on a small batch takes
 # longer here than on the GPU.)
 _DTYPE_CODES = {torch.float32: ESA_F32, torch.bfloat16: ESA_BF16}
-_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _q8_call(cache: CacheQ8, where: str, *args):
@@ -529,13 +529,6 @@ def _q8_dtype(t: torch.Tensor) -> int:
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     return code
-
-
-def _q8_empty(shape, dtype, cache: CacheQ8) -> torch.Tensor:
-    """torch.empty of a shape of 3 or 4 (empty_strided takes half its host time)."""
-    n = shape[-1]
-    strides = (shape[1] * n, n, 1) if len(shape) == 3 else (shape[1] * shape[2] * n, shape[2] * n, n, 1)
-    return torch.empty_strided(shape, strides, dtype=dtype, device=cache._k.device)
 
 
 def _q8_tensor(t: torch.Tensor, name: str, cache: CacheQ8, dtype, shape) -> int:
@@ -607,14 +600,18 @@ def cache_read_q8(cache: CacheQ8, start: int = 0, rows: Optional[int] = None, id
     if not want_k:
         k_out = None
     elif k_out is None:
-        k_out = _q8_empty(shape, dtype, cache)
+        # (empty_strided and empty_like take two thirds of torch.empty's host time)
+        k_out = torch.empty_strided(shape, (n * h * d, h * d, d, 1), dtype=dtype, device=cache._k.device)
         kp = k_out.data_ptr()
     else:
         kp = _q8_tensor(k_out, "k_out", cache, dtype, shape)
     if not want_v:
         v_out = None
     elif v_out is None:
-        v_out = _q8_empty(shape, dtype, cache)
+        if kp is not None:
+            v_out = torch.empty_like(k_out)
+        else:
+            v_out = torch.empty_strided(shape, (n * h * d, h * d, d, 1), dtype=dtype, device=cache._k.device)
         vp = v_out.data_ptr()
     else:
         vp = _q8_tensor(v_out, "v_out", cache, dtype, shape)
@@ -648,7 +645,7 @@ def _q8_attn(q, cache: CacheQ8, idx, count, p: EsaParams, want_lse, out, lse):
     if not want_lse:
         lse = None
     elif lse is None:
-        lse = _q8_empty(shape[:3], torch.float32, cache)
+        lse = cache._k_scale.new_empty(b, shape[1], shape[2])
         lp = lse.data_ptr()
     else:
         lp = _q8_tensor(lse, "lse", cache, torch.float32, shape[:3])
