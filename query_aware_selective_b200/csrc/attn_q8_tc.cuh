@@ -32,7 +32,9 @@
 // to the launch, the queries and the first keys, 1.8 us to the last tile and the merge, and
 // 128 units leave 20 of 148 SMs idle. One CTA of six stages an SM beat two of three, 39.7
 // against 42 us. With more rows bound by the softmax warps' issue slots: 20 rows x 24 units
-// (39 MB) take 23 us, a tile of 128 keys 2650 cycles. (Converted to f16 for mma.sync, as
+// (39 MB) take 20.7 us, a tile of 128 keys 2400 cycles (12 warps in step: 340 waiting for
+// barriers that are complete, 850 to the tile's maxima, 800 for weights and pieces, 450 each
+// to store them and to read O). (Converted to f16 for mma.sync, as
 // attn_q8.cuh does, the same keys took 70 and 77 us: the conversions cost more issue slots
 // than the softmax.)
 #pragma once

@@ -1288,18 +1288,18 @@ int q8_box_group(int g) { return std::min(g & -g, esa::kTcRows); }
 // whole list: 60 to 65 us for 6.3K keys whatever the rows, until its CTAs outnumber the SMs,
 // and 0.8 us of staging for every sequence and KV head of 128) or runs on the codes.
 // Heads of 128: attn_q8_tc_kernel splits each list over clusters while its units of work
-// (sequence, KV head, 24 rows) leave SMs free for that: 22 us for 24 units, 44 with up to 74,
-// 75 to 80 with up to 148, a wave more for each further 148; with 8 heads on 40 and one
-// sequence, 130 rows (48 units) 42 us against 67 staged, 255 rows (88) 75 against 67, 2560
-// rows 451 against 132. So: codes up to half the SMs' number of units, and under 64 rows,
-// whose 128-row tiles would be half empty. Heads of 64: attn_q8_kernel takes 16 rows a unit,
-// 62 us for 224 units against 70 staged, 92 for 416 against 71, 220 for 1024 against 68, and
-// with 128 (sequence, KV head)s 69 us for 20 rows against 109, 133 for 52 against 109.
+// (sequence, KV head, 24 rows) leave SMs free for that: 21 us for 24 units, 40 with up to 74,
+// 70 with up to 148 (85 staged for 4 sequences of 65 rows, 67 for one of 255), a wave more for
+// each further 148: 134 for 192 units against 109, 217 for 384 against 171, 451 against 132
+// for 512 queries of 5 heads a KV head. Up to 48 rows (two tiles) it keeps the lead: 138
+// against 171 for 128 (sequence, KV head)s of 40. Heads of 64: attn_q8_kernel takes 16 rows a
+// unit, 62 us for 224 units against 70 staged, 92 for 416 against 71, 220 for 1024 against
+// 68, and with 128 (sequence, KV head)s 69 us for 20 rows against 109, 133 for 52 against 109.
 bool q8_chunk_form(int64_t batch, int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
   const int g = hq / hkv;
   const int64_t rows = (int64_t)lq * g, n = batch * hkv;
   if (dt != ESA_BF16) return false;
-  if (head_dim == 128) return rows >= 64 && n * q8_row_tiles(rows) > 74;
+  if (head_dim == 128) return rows > 48 && n * q8_row_tiles(rows) > 148;
   return (int64_t)lq * q8_box_group(g) > 32 && n * cdiv(rows, 16) > 296;
 }
 

@@ -414,11 +414,11 @@ def test_attention_few_queries(fmt, dtype, b, lq, n_cap, hq, hkv, d, block, list
     (False, 1, 33, 1300, 4, 2, 128, 1, 128, 512, 100),           # G 2
     (False, 1, 8, 700, 16, 2, 32, 1, 0, 0, 64),                  # G 8, no initial tokens, no window
     (False, 1, 300, 300, 4, 1, 64, 1, 16, 64, 32),               # the first chunk: nothing before it
-    (True, 1, 256, 1500, 8, 8, 64, 1, 32, 256, 300),             # the same on the chunk form
-    (True, 2, 130, 1200, 8, 2, 16, 2, 16, 200, 150),
-    (True, 1, 460, 1300, 4, 2, 128, 1, 128, 512, 100),
-    (True, 1, 120, 700, 16, 2, 32, 1, 0, 0, 64),
-    (True, 1, 460, 460, 4, 1, 64, 1, 16, 64, 32),
+    (True, 1, 450, 1500, 8, 8, 64, 1, 32, 256, 300),             # the same on the chunk form
+    (True, 2, 230, 1200, 8, 2, 16, 2, 16, 200, 150),
+    (True, 1, 900, 1300, 4, 2, 128, 1, 128, 512, 100),
+    (True, 1, 230, 700, 16, 2, 32, 1, 0, 0, 64),
+    (True, 1, 900, 900, 4, 1, 64, 1, 16, 64, 32),
 ])
 def test_attention_chunk(fmt, chunk, b, lq, n_cap, hq, hkv, block, lists, n_init, window, topk):
     d = 128
