@@ -1309,13 +1309,18 @@ int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
   return cdiv(r.ni + p.topk + (c0 - r.lo) + lq, esa::kTcKeys) * esa::kTcKeys;
 }
 
-// The largest cluster of up to 8 CTAs (and up to `most`) with which `units` units of work, a
-// cluster each, all run at once: clusters split a unit's keys, a second wave would cost
-// what they save (24 units x 6 CTAs of one per SM left 8 CTAs to a second wave, 44 against
-// 25 us; fp32 on 128 units, one CTA per SM: 53 us without clusters, 60 with two CTAs). How
-// many clusters of 2 .. 8 fit is asked once per kernel and context (a byte each).
+// The size of the clusters, up to 8 CTAs (and up to `most`), that split the keys of `units`
+// units of work, a cluster each. A wave of clusters takes what starting, merging and ending a
+// CTA do, about as much as 1024 keys, and each CTA's share of the n_keys; the size with the
+// least sum over the waves is taken, more waves of larger ones if that gains a tenth. While all
+// clusters run at once that is the largest that still does (24 units of 6.3K keys: 5 CTAs 21 us; 6,
+// which left 8 CTAs to a second wave, 44 against 25 when one wave took that); 88 units in 2
+// waves of clusters of 3 take 57 us, 68 without clusters; 152 in 3 waves of 2 70, 74 in 2
+// waves without; 512 in 4 waves 153, 164 in 7 of 2 (without the tenth). How many fit at once
+// is asked once per kernel and context (a byte each: CTAs an SM, clusters of 2 .. 8).
 template <typename Kernel>
-esa_status_t q8_cluster_size(Kernel kernel, int threads, int smem, int64_t units, int64_t most, int* csize) {
+esa_status_t q8_cluster_size(Kernel kernel, int threads, int smem, int64_t units, int64_t n_keys, int64_t most,
+                             int* csize) {
   intptr_t fit = 0;
   const esa_status_t st = per_context(reinterpret_cast<const void*>(kernel), &fit, [&](intptr_t* v) {
     ESA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -1333,14 +1338,26 @@ esa_status_t q8_cluster_size(Kernel kernel, int threads, int smem, int64_t units
       q.numAttrs = 1;
       int n = 0;
       ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &q));
-      *v |= (intptr_t)std::min(n, 255) << (8 * (c - 2));
+      *v |= (intptr_t)std::min(n, 255) << (8 * (c - 1));
     }
+    int per_sm = 0;
+    ESA_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem));
+    *v |= per_sm;
     return ESA_OK;
   });
   if (st != ESA_OK) return st;
   *csize = 1;
-  for (int c = 2; c <= 8 && c <= most; ++c)
-    if (units <= ((fit >> (8 * (c - 2))) & 255)) *csize = c;
+  double least = 0;
+  for (int c = 1; c <= 8 && (c == 1 || c <= most); ++c) {
+    const int64_t at_once = c == 1 ? (fit & 255) * 148 : (fit >> (8 * (c - 1))) & 255;
+    if (at_once == 0) continue;
+    const int64_t waves = cdiv(units, at_once);
+    const double cost = (double)waves * (1024 + (double)n_keys / c);
+    if (c == 1 || cost < (waves == 1 ? 1. : 0.9) * least) {
+      least = cost;
+      *csize = c;
+    }
+  }
   return ESA_OK;
 }
 
@@ -1352,7 +1369,7 @@ esa_status_t launch_attn_q8(esa::AttnQ8Args a, int32_t batch, int64_t n_keys, cu
   if (tiles * a.hkv > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
   a.tiles = (int)tiles;
   int csize;
-  esa_status_t st = q8_cluster_size(kernel, esa::kQ8Threads, smem, (int64_t)batch * a.hkv * tiles,
+  esa_status_t st = q8_cluster_size(kernel, esa::kQ8Threads, smem, (int64_t)batch * a.hkv * tiles, n_keys,
                                     cdiv(n_keys, esa::kQ8Keys * esa::kQ8Warps), &csize);
   if (st != ESA_OK) return st;
   st = launch_q8(kernel, "attn_q8_kernel", dim3(csize, a.hkv * a.tiles, batch), esa::kQ8Threads, smem, csize, s, a);
@@ -1376,7 +1393,7 @@ esa_status_t launch_attn_q8_tc(esa::AttnQ8Args a, int32_t batch, int64_t n_keys,
   if (tiles * a.hkv > 65535) return fail(ESA_ERR_UNSUPPORTED, "more than 65535 row tiles");
   a.tiles = (int)tiles;
   int csize;
-  esa_status_t st = q8_cluster_size(kernel, Sh::kThreads, Sh::kSmem, (int64_t)batch * a.hkv * tiles,
+  esa_status_t st = q8_cluster_size(kernel, Sh::kThreads, Sh::kSmem, (int64_t)batch * a.hkv * tiles, n_keys,
                                     cdiv(n_keys, esa::kQtKeys), &csize);
   if (st != ESA_OK) return st;
   st = launch_q8(kernel, "attn_q8_tc_kernel", dim3(csize, a.hkv * a.tiles, batch), Sh::kThreads, Sh::kSmem, csize, s, a);

@@ -432,6 +432,37 @@ def test_attention_chunk(fmt, chunk, b, lq, n_cap, hq, hkv, block, lists, n_init
     _check(o, lse, _reference(q, kv, vv, [c0] * b, idx, cnt, n_init, window), torch.bfloat16, d, chunk=chunk)
 
 
+@pytest.mark.parametrize("b,lq,d", [(19, 1, 128), (11, 13, 128), (38, 1, 64)])
+def test_attention_more_units_than_run_at_once(b, lq, d):
+    """Long lists of more (sequence, KV head)s than the SMs hold: clusters in several waves. The
+    reference is formed on the GPU, in 64 bits."""
+    n, hq, hkv, block = 6000, 16, 8, 64
+    g = torch.Generator(device=DEV).manual_seed(7)
+    parts = []
+    for _ in range(2):
+        parts.append(torch.randint(-127, 128, (b, n, hkv, d), generator=g, device=DEV, dtype=torch.int8))
+        parts.append(torch.exp2(torch.randint(-9, -5, (b, -(-n // block), hkv), generator=g, device=DEV).float()))
+    cache = qas.CacheQ8(*parts, block)
+    q = torch.randn((b, lq, hq, d), generator=g, device=DEV).to(torch.bfloat16)
+    p = qas.params(0, n, 1, 0)
+    idx, cnt = torch.zeros((b, 1), dtype=torch.int32, device=DEV), torch.zeros(b, dtype=torch.int32, device=DEV)
+    assert qas._abi.sparse_attn_q8_workspace_size(b, lq, n - lq, hq, hkv, d, 1, p) == 0
+    o, lse = qas.sparse_attn_q8(q, cache, n - lq, idx, cnt, p, want_lse=True)
+    blk = torch.arange(n, device=DEV) // block
+    late = torch.arange(n, device=DEV)[None, :] > n - lq + torch.arange(lq, device=DEV)[:, None]
+    ref = [[] for _ in range(5)]
+    for s in range(b):
+        k, v = (parts[i][s].double() * parts[i + 1][s, blk].double()[..., None] for i in (0, 2))
+        k, v = (t.permute(1, 0, 2).repeat_interleave(hq // hkv, dim=0) for t in (k, v))           # [Hq, n, D]
+        qq = q[s].double().permute(1, 0, 2)                                                       # [Hq, Lq, D]
+        x = (qq @ k.transpose(1, 2) * d ** -0.5).masked_fill(late, -float("inf"))
+        w, big = x.softmax(dim=2), (qq.abs() @ k.abs().transpose(1, 2) * d ** -0.5).masked_fill(late, 0.0)
+        least = (~late).double() @ v.abs() * w.amax(dim=2, keepdim=True)
+        for at, t in zip(ref, (w @ v, x.logsumexp(dim=2), w @ v.abs(), big.amax(dim=2), least)):
+            at.append(t.transpose(0, 1).cpu().numpy())
+    _check(o, lse, [np.stack(t) for t in ref], torch.bfloat16, d)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("chunk,b,lq,n_cap,hq,hkv,d,block,lists,n_init,window,topk", [
     (True, 2, 210, 1100, 10, 2, 128, 32, 2, 16, 200, 150),       # G 5, gathered queries, a list per head, ragged
