@@ -925,3 +925,22 @@ def test_decode_step_in_a_graph_with_lengths_that_differ():
         kv, vv = _values(c.cache)
         _check(c.out, None, _reference(q.cpu(), kv, vv, [int(x) - 1 for x in nc], c.idx.cpu(), c.count.cpu(), 32, 64),
                torch.bfloat16, d)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,chunk", [(torch.bfloat16, 28, 4, 256), (torch.float32, 4, 4, 160)])
+def test_prefill_over_a_cache_of_heads_of_64(dtype, hq, hkv, chunk):
+    b, n, d, dc, n_init, window, topk = 2, 600, 64, 64, 32, 64, 90
+    g = torch.Generator().manual_seed(15)
+    q, k, v = (torch.randn((b, n, h, d), generator=g).to(dtype) for h in (hq, hkv, hkv))
+    wq, wk = (torch.randn((hq * d, dc), generator=g).to(DEV) / 32 for _ in range(2))
+    p = qas.params(n_init, window, topk, 2, 45.25)
+    cache = _cache(b, n + 8, hkv, d, "e4m3", 16)
+    pf = pipeline.EsaPrefill(b, n, chunk, hq, hkv, d, dc, p, dtype=dtype, cache=cache)
+    out = pf.run(q.to(DEV), k.to(DEV), v.to(DEV), wq, wk)
+    kv, vv = _values(cache)
+    for ci, (c0, lq) in enumerate(pf.chunks()):
+        idx, cnt = pf.idx_all[ci].cpu().view(b, 1, topk), pf.count_all[ci].cpu().view(b, 1)
+        ws = qas._abi.sparse_attn_q8_workspace_size(b, lq, c0, hq, hkv, d, int(dtype == torch.bfloat16), p)
+        assert (ws > 0) == (dtype == torch.bfloat16)
+        _check(out[:, c0:c0 + lq], None, _reference(q[:, c0:c0 + lq], kv, vv, [c0] * b, idx, cnt, n_init, window), dtype,
+               d, chunk=ws > 0)
