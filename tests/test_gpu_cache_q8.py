@@ -944,3 +944,54 @@ def test_prefill_over_a_cache_of_heads_of_64(dtype, hq, hkv, chunk):
         assert (ws > 0) == (dtype == torch.bfloat16)
         _check(out[:, c0:c0 + lq], None, _reference(q[:, c0:c0 + lq], kv, vv, [c0] * b, idx, cnt, n_init, window), dtype,
                d, chunk=ws > 0)
+
+
+def test_captured_behind_copies_and_joined_streams():
+    """Each call as the first kernel behind a copy, a fill and the join of two streams: its inputs
+    are those that the graph's nodes before it wrote."""
+    b, n_cap, hq, hkv, d = 2, 300, 8, 2, 128
+    p = qas.params(8, 64, 50, 0)
+    q, k, v = (torch.randn((b, 3, h, d), device=DEV).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    seq_len = torch.tensor([150, 260], device=DEV)
+    idx = torch.arange(8, 58, dtype=torch.int32, device=DEV).repeat(b, 1)
+    cnt = torch.full((b,), 50, dtype=torch.int32, device=DEV)
+    start, _, _ = _filled(b, n_cap, hkv, d, "e4m3", 32, [n_cap] * b, 971)
+    work = qas.cache_q8(b, n_cap, hkv, d, torch.float8_e4m3fn, 32, device=DEV)
+    qi, ki, vi, li = (torch.zeros_like(t) for t in (q, k, v, seq_len))
+
+    def reset():
+        for t, u in ((work.k, start.k), (work.v, start.v)):
+            t.view(torch.uint8).copy_(u.view(torch.uint8))
+        work.k_scale.copy_(start.k_scale)
+        work.v_scale.copy_(start.v_scale)
+
+    def step():
+        ki.copy_(k)
+        vi.copy_(v)
+        li.copy_(seq_len)
+        qas.cache_write_q8_varlen(work, ki, vi, li)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            qi.copy_(q)
+        torch.cuda.current_stream().wait_stream(side)
+        o, lse = qas.sparse_attn_q8_varlen(qi[:, :1].contiguous(), work, li, idx, cnt, p, want_lse=True)
+        li.zero_()
+        return o, lse, *qas.cache_read_q8(work, start=100, rows=170)
+    side = torch.cuda.Stream()
+    reset()
+    want = [t.clone() for t in step()]
+    for t in (qi, ki, vi, li):
+        t.zero_()
+    reset()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        reset()
+        for t in (*got, qi, ki, vi, li):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    qas.device_status()
