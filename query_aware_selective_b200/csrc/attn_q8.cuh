@@ -554,21 +554,23 @@ struct Q8TcProblem : EsaTcProblem {
   int d;
   int parts;             // G is that of a part, blockIdx.y counts parts
   bool boxed;            // Q tiles are boxes
+  int kvh;               // per CTA: the KV head
   __device__ bool setup() {
     tile = blockIdx.x;
     g = blockIdx.y;
     b = blockIdx.z;
     if (tile * kTcRows >= lq * G) return false;
-    list = lists > 1 ? b * lists + g / parts : b;              // the list of the part's KV head
+    kvh = g / parts;
+    list = lists > 1 ? b * lists + kvh : b;
     cnt = min(max(keys.count[list], 0), (int)keys.idx_stride);
     n_prior = keys.ni + cnt + (c0 - keys.lo);
     nk = n_prior + min(lq - 1, (tile * kTcRows + kTcRows - 1) / G) + 1;
     return true;
   }
   __device__ bool q_box(int* y, int* z) const { return boxed && EsaTcProblem::q_box(y, z); }
-  __device__ int32_t kv_row(int64_t t) const { return (int32_t)(((int64_t)b * t_pad + t) * hkv + g / parts); }
+  __device__ int32_t kv_row(int64_t t) const { return (int32_t)(((int64_t)b * t_pad + t) * hkv + kvh); }
   __device__ int kv_box(int j, int* y, int* z) const {
-    *y = g / parts;
+    *y = kvh;
     *z = (int)((int64_t)b * t_pad + (int64_t)j * kTcKeys);
     return 1;
   }
