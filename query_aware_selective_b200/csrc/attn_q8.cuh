@@ -17,9 +17,12 @@
 // side by side (prmt), and one conversion per two codes. S^T becomes the B operand of the
 // second product by movmatrix.
 // m is a reference, not the maximum: it is raised to max_j (x_j + log2 b_j) when that
-// exceeds it by 5, and W = 2^(x_j + log2 b_j - m + 10) <= 2^15 is rounded to f16 (relative
+// exceeds it by 5, and W = e_j b_j 2^10 <= 2^15, e_j = 2^(x_j - m), is rounded to f16 (relative
 // 2^-11; a weight under 2^-35 of the largest is lost, which 2^20 of them do not make
-// visible). l sums the unrounded W 2^-10 / b_j. fp32 queries go in as two f16 (q = hi +
+// visible). l sums the e_j, which hold no b_j: from W it would lose the keys whose values are
+// zero (b_j 2^-100) beside loud ones. e_j spans 2^105 (those keys) down to 2^-98 for the row's
+// largest x_j (under values of 2^97), and a step of m the sum of the two, more than one
+// exponential holds: l takes it as two halves. fp32 queries go in as two f16 (q = hi +
 // lo), and so do the weights, for 22 bits of each: more bits than 8-bit pieces give in a
 // narrow MMA, which is why fp32 stays here; a head of 64 is half the M = 128 that the
 // 8-bit MMAs of attn_q8_tc.cuh take.
@@ -44,7 +47,8 @@ namespace esa {
 constexpr int kQ8Warps = 8, kQ8Threads = kQ8Warps * 32;
 constexpr int kQ8Keys = 16;                     // keys of a warp's step
 constexpr int kQ8Stages = 3;                    // steps of a warp's ring
-constexpr float kQ8Head = 10.f, kQ8Most = 0x1p15f;  // weights: 2^10 at the reference, at most 2^15 (f16: 2^16)
+// weights: 2^10 at the reference, at most 2^15 (f16: 2^16)
+constexpr float kQ8Head = 10.f, kQ8Unit = 0x1p10f, kQ8Most = 0x1p15f;
 
 struct AttnQ8Args {
   const void* q;            // [B, Lq, Hq, D]
@@ -156,10 +160,20 @@ __device__ __forceinline__ void q8_transpose(uint32_t wa, uint32_t wb, uint32_t*
   }
 }
 
-// log2 of a value block's scale (within 2^-23 at powers of two; the weights' reciprocal
-// factors are taken from it). Scales under the least that is written, zero among them, count
-// as that: 2^100 times 2^27 tokens still fit a row sum.
-__device__ __forceinline__ float q8_scale_log2(float s) { return __log2f(s < 0x1p-100f ? 0x1p-100f : s); }
+// log2 of a normal number
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The scales of a key as the softmax takes them. Scales of values under the least that is
+// written, zero among them, count as that: 2^100 times 2^22 tokens still fit a row sum behind
+// an m that is 5 low. One that is no finite number makes NaN of the rows that attend the key
+// (through its logit), and of no others (their weight is a finite number times 0).
+__device__ __forceinline__ void q8_scales(float& k, float& v) {
+  k = fmaf(v, 0.f, k);
+  v = fminf(fmaxf(v, 0x1p-100f), 0x1p100f);
+}
 
 // The exponent of a power of two that brings amax to [2^13, 2^14): queries of any range
 // fit f16, and the elements that matter stay normal there.
@@ -359,18 +373,21 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
     // softmax: keys gid and gid + 8 (u), rows 2 tig and 2 tig + 1 (j). The weights come
     // first, against m as it is; the row maxima (a reduction over 8 lanes) only when one of
     // them says that m has to rise (at once on the first step: m is -inf).
-    float ka[2], lv[2];
+    float ka[2], vb[2];                  // scales of the two keys, the values' times 2^10
     {
-      const float lg = q8_scale_log2(sc_cur);
+      const float other = __shfl_xor_sync(0xffffffffu, sc_cur, 16);
+      float ks = sc_cur, vs = lane < 16 ? other : sc_cur;
+      q8_scales(ks, vs);
+      const float own = lane < 16 ? ks : vs * kQ8Unit;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        ka[u] = __shfl_sync(0xffffffffu, sc_cur, gid + 8 * u);
-        lv[u] = __shfl_sync(0xffffffffu, lg, 16 + gid + 8 * u) + kQ8Head;
+        ka[u] = __shfl_sync(0xffffffffu, own, gid + 8 * u);
+        vb[u] = __shfl_sync(0xffffffffu, own, 16 + gid + 8 * u);
       }
     }
     const int t0 = s * kQ8Keys;
     const bool cut = t0 + kQ8Keys > n_all;                     // some row does not see some key
-    float wt[NT][2][2];
+    float ex[NT][2][2], wt[NT][2][2];
     auto weights = [&]() -> float {
       float top = 0.f;
 #pragma unroll
@@ -378,8 +395,10 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            wt[nt][u][j] = fast_exp2(fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], lv[u] - m[nt][j]));
+          for (int u = 0; u < 2; ++u) {
+            ex[nt][u][j] = fast_exp2(fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], -m[nt][j]));
+            wt[nt][u][j] = ex[nt][u][j] * vb[u];
+          }
       if (cut) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -387,7 +406,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              if (t0 + gid + 8 * u >= lim[nt][j]) wt[nt][u][j] = 0.f;
+              if (t0 + gid + 8 * u >= lim[nt][j]) ex[nt][u][j] = wt[nt][u][j] = 0.f;
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -395,6 +414,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
       return top;
     };
     if (__any_sync(0xffffffffu, weights() > kQ8Most)) {
+      const float lv[2] = {fast_log2(vb[0]) - kQ8Head, fast_log2(vb[1]) - kQ8Head};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float al[2];
@@ -403,16 +423,17 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
           float mx = -INFINITY;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float x = fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], lv[u] - kQ8Head);
+            const float x = fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], lv[u]);
             if (t0 + gid + 8 * u < lim[nt][j]) mx = fmaxf(mx, x);
           }
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           const float mn = fmaxf(m[nt][j], mx);
-          al[j] = mn == -INFINITY ? 1.f : fast_exp2(m[nt][j] - mn);
+          const float half = mn == -INFINITY ? 1.f : fast_exp2(0.5f * (m[nt][j] - mn));
+          al[j] = half * half;
           m[nt][j] = mn;
-          l[nt][j] *= al[j];
+          l[nt][j] = l[nt][j] * half * half;
         }
 #pragma unroll
         for (int t = 0; t < 2 * VW; ++t) {
@@ -425,13 +446,12 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
       weights();
     }
     uint32_t wf[NT][2], wl[F32 ? NT : 1][2];
-    const float iv[2] = {fast_exp2(-lv[0]), fast_exp2(-lv[1])};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) l[nt][j] = fmaf(wt[nt][u][j], iv[u], l[nt][j]);
+        for (int j = 0; j < 2; ++j) l[nt][j] += ex[nt][u][j];
         const uint32_t h = f16x2_rn(wt[nt][u][0], wt[nt][u][1]);
         wf[nt][u] = movmatrix_t(h);
         if constexpr (F32) {
@@ -501,9 +521,9 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
 #pragma unroll
     for (int u = 0; u < kQ8Warps; ++u) {
       const int wr = u * ROWS + r;
-      const float c = fast_exp2(sm_ml[wr * 2] - mr);
+      const float half = fast_exp2(0.5f * (sm_ml[wr * 2] - mr)), c = half * half;
       const float4 o = *reinterpret_cast<const float4*>(sm_o + wr * RF + d4 * 4);
-      L += sm_ml[wr * 2 + 1] * c;
+      L += sm_ml[wr * 2 + 1] * half * half;
       O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
     }
     *reinterpret_cast<float4*>(sm_o + r * RF + d4 * 4) = O;                  // read by this thread only
@@ -523,13 +543,13 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
     for (int u = 0; u < csize; ++u) {
       const uint2 z = ld_dsmem_u2(dsmem_map(ml, u));
       const float4 o = ld_dsmem_f4(dsmem_map(oo, u));
-      const float c = fast_exp2(__uint_as_float(z.x) - mr);
-      L += __uint_as_float(z.y) * c;
+      const float half = fast_exp2(0.5f * (__uint_as_float(z.x) - mr)), c = half * half;
+      L += __uint_as_float(z.y) * half * half;
       O.x += o.x * c; O.y += o.y * c; O.z += o.z * c; O.w += o.w * c;
     }
     const int i = a.lq == 1 ? 0 : (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
     const int64_t row = ((int64_t)b * a.lq + i) * a.hq + g * a.G + hl;
-    const float inv = 0x1p-10f / L;                                          // 2^-kQ8Head
+    const float inv = 1.f / kQ8Unit / L;
     T* dst = static_cast<T*>(a.o) + row * D + d4 * 4;
     if constexpr (F32) {
       *reinterpret_cast<float4*>(dst) = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);

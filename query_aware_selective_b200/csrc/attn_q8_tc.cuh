@@ -18,7 +18,9 @@
 // is drained from TMEM into fp32 registers and scaled there: the range of 8-bit pieces
 // then only has to span one tile (a weight is rounded to 2^-26 (e4m3) or 2^-28 (int8) of its
 // tile's largest at worst; three int8 digits, 2^-21, showed in dims where the largest
-// weight's value is next to zero), and nothing in TMEM is ever rescaled.
+// weight's value is next to zero), and nothing in TMEM is ever rescaled. The maximum is
+// that of x_j + log2 b_j, and a weight e_j b_j with e_j = 2^(x_j - maximum); l sums the e_j (as in
+// attn_q8.cuh: b_j spans 2^198, which a weight does not hold).
 //
 // Roles: one to three softmax warpgroups (thread = key for S and W, thread = dim for O; up to
 // 8 query rows each, and with few rows two that take turns at the key tiles), one warp that
@@ -240,8 +242,8 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
   constexpr int RT = Sh::RT, N = Sh::N, NST = Sh::kStages, NS = Sh::NS, NQ = Sh::NQ, NW = Sh::NW;
   constexpr int kMmaWarp = 4 * RG * TG, kProdWarp = kMmaWarp + 1, kSoftThreads = 128 * RG * TG;
   constexpr int kBarTmem = RG * TG + 1, kBarQ = RG * TG + 2;      // named barriers (1 .. RG * TG: the warpgroups)
-  // a weight of 1 (its tile's largest) goes in as 2^8 (e4m3, <= 448), 2^27 (int8, <= 127 * 2^21)
-  constexpr float kTop = FMT == kQ8E4M3 ? 8.f : 27.f;
+  // a tile's largest weight goes in as 2^8 (e4m3, <= 448), 2^27 (int8, <= 127 * 2^21)
+  constexpr float kTop = FMT == kQ8E4M3 ? 0x1p8f : 0x1p27f;
   // units of q8_join for a query and for a weight
   constexpr float kUnitQ = FMT == kQ8E4M3 ? 1.f : 0x1p14f, kUnitW = FMT == kQ8E4M3 ? 1.f : 0x1p14f;
   extern __shared__ __align__(1024) uint8_t qtsm[];
@@ -527,13 +529,13 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       tc_fence_after();
       float x[WR];
       const float* sc = reinterpret_cast<const float*>(qtsm + (j % NST) * kQtStage + 2 * kQtTile);
-      const float ka = sc[key];
-      const float lv = q8_scale_log2(sc[kQtKeys + key]);
+      float ka = sc[key], vb = sc[kQtKeys + key];
+      q8_scales(ka, vb);
       {
         uint32_t v[NQ * WR];
         tmem_ld_cols(lane_base + (j % NS) * N, v);
 #pragma unroll
-        for (int r = 0; r < WR; ++r) x[r] = fmaf(q8_join<FMT, WR, NQ>(v, r), ka * xs[r], lv);
+        for (int r = 0; r < WR; ++r) x[r] = q8_join<FMT, WR, NQ>(v, r) * (ka * xs[r]);
       }
       const int t0 = slot_t(j, 0);
       if (t0 + kQtKeys > n_all) {
@@ -541,14 +543,15 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
         for (int r = 0; r < WR; ++r)
           if (t0 + key >= n_prior + min(r0 + row_wg + r, a.lq * a.G - 1) / a.G + 1) x[r] = -INFINITY;
       }
-      // the tile's maximum of each row
+      // the tile's maximum of each row, of logit and value scale together
       // [warp][RT]; two buffers in turn: a warp that writes one has passed the barrier of the
       // tile in between, and with it every warp's reads of the maxima before that
       float* mx = smf + Sh::kMax + (2 * tg + ((j / TG) & 1)) * 4 * RT + row_wg;
       {
         float mw[WR];
+        const float lv = fast_log2(vb);
 #pragma unroll
-        for (int r = 0; r < WR; ++r) mw[r] = redux_max(x[r]);
+        for (int r = 0; r < WR; ++r) mw[r] = redux_max(x[r] + lv);
         if (lane == 0) {
 #pragma unroll
           for (int r = 0; r < WR; r += 4)
@@ -562,16 +565,23 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       // a named barrier has no time limit: the four warps leave together if a wait ran out
       if (!(ok = bar_all(bar_wg, 128, ok))) break;
       const float mt = fmaxf(fmaxf(mx[row_own], mx[RT + row_own]), fmaxf(mx[2 * RT + row_own], mx[3 * RT + row_own]));
-      const float top = (mt == -INFINITY ? 0.f : mt) - kTop;
+      const float top = mt == -INFINITY ? 0.f : mt;
+      const float mn = fmaxf(m, mt), mr = mn == -INFINITY ? 0.f : mn;
+      const float al_own = fast_exp2(m - mr), be_own = fast_exp2(mt - mr);                       // (one of them is 1)
+      const bool far = __any_sync(0xffffffffu, al_own * be_own < 0x1p-120f && m > -INFINITY);
       // weights, as pieces, to this key's row of the W buffer: [16 columns][128 keys][16 bytes]
-      const float iv = fast_exp2(-lv - kTop);
+      const float unit = vb * kTop;
       uint32_t ww[NW + 1][WR / 4];
 #pragma unroll
       for (int r = 0; r < WR; r += 4) {
         uint32_t pc[NW];
+        float w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[r + u] = fast_exp2(x[r + u] - __shfl_sync(0xffffffffu, top, r + u));
-        q8_split4<FMT, NW>(x + r, pc);
+        for (int u = 0; u < 4; ++u) {
+          x[r + u] = fast_exp2(x[r + u] - __shfl_sync(0xffffffffu, top, r + u));
+          w[u] = x[r + u] * unit;
+        }
+        q8_split4<FMT, NW>(w, pc);
 #pragma unroll
         for (int p = 0; p < NW; ++p) ww[p][r / 4] = pc[p];
         ww[NW][r / 4] = 0u;
@@ -591,15 +601,25 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       tc_fence_before();
       mbar_arrive_warp(&sm.w_full[j & 1]);
       if (TG == 1 && j >= TG) ok = ok && drain(j - TG);
-      const float mn = fmaxf(m, mt), mr = mn == -INFINITY ? 0.f : mn;
-      const float al_own = fast_exp2(m - mr), be_own = fast_exp2(mt - mr);
-      m = mn;
 #pragma unroll
       for (int r = 0; r < WR; ++r) {
         al[r] = __shfl_sync(0xffffffffu, al_own, r);
         be[r] = __shfl_sync(0xffffffffu, be_own, r);
-        l[r] = fmaf(l[r], al[r], x[r] * iv * be[r]);
       }
+      if (__builtin_expect(far, 0)) {
+        // a factor that an exponential does not hold, though its product with the sum may be
+        // any number: as two halves
+        const float ah = fast_exp2(0.5f * (m - mr)), bh = fast_exp2(0.5f * (mt - mr));
+#pragma unroll
+        for (int r = 0; r < WR; ++r) {
+          const float a = __shfl_sync(0xffffffffu, ah, r), c = __shfl_sync(0xffffffffu, bh, r);
+          l[r] = fmaf(l[r] * a, a, x[r] * c * c);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < WR; ++r) l[r] = fmaf(l[r], al[r], x[r] * be[r]);
+      }
+      m = mn;
     }
     const int last = (nt - 1 - tg) / TG * TG + tg;  // the warpgroup's last tile, if it had one
     if (tg < nt && ok) ok = drain(last);
@@ -650,13 +670,13 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     for (int u = 0; u < parts; ++u) {
       const float2 z = *reinterpret_cast<const float2*>(ml + u * RT * 2);
       const float4 x = *reinterpret_cast<const float4*>(po + u * per);
-      const float c = fast_exp2(z.x - (M == -INFINITY ? 0.f : M));
-      L += z.y * c;
+      const float half = fast_exp2(0.5f * (z.x - (M == -INFINITY ? 0.f : M))), c = half * half;
+      L += z.y * half * half;
       O.x += x.x * c; O.y += x.y * c; O.z += x.z * c; O.w += x.w * c;
     }
     const int i = a.lq == 1 ? 0 : (r0 + r) / a.G, hl = (r0 + r) - i * a.G;
     const int64_t row = ((int64_t)b * a.lq + i) * a.hq + g * a.G + hl;
-    const float inv = (FMT == kQ8E4M3 ? 0x1p-8f : 0x1p-27f) * kUnitW / L;
+    const float inv = kUnitW / kTop / L;
     uint2 w;
     w.x = bf16x2_rn(O.x * inv, O.y * inv);
     w.y = bf16x2_rn(O.z * inv, O.w * inv);

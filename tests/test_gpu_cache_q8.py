@@ -693,6 +693,61 @@ def test_attention_nan_and_infinity_stay_in_their_rows(fmt, dtype, d, lq):
     qas.device_status()
 
 
+def _loud_keys(layout, n, block):
+    """Which of n tokens have loud values, the others zeros: whole tiles of 128 keys behind or
+    ahead of quiet ones, tiles in turn, blocks inside a tile in turn, one token alone."""
+    t = torch.arange(n)
+    return {"behind": t >= n // 2, "ahead": t < n // 2, "tiles": t // 128 % 2 == 1, "blocks": t // block % 2 == 0,
+            "one": t == n - 1, "first": t == 0}[layout]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("exponent", [27, 60, 97])
+@pytest.mark.parametrize("dtype,d,lq", [(torch.bfloat16, 128, 1), (torch.bfloat16, 128, 5), (torch.float32, 128, 1),
+                                        (torch.float32, 64, 3), (torch.bfloat16, 64, 1)])
+def test_attention_zero_values_beside_loud_ones(fmt, exponent, dtype, d, lq):
+    """A key whose values are zero (scale 2^-100) counts in the sum of the weights as much as one
+    whose values are near the largest that is allowed, wherever the two lie."""
+    n, block, group = 1024, 32, 4
+    p = qas.params(0, n, 1, 0)
+    for hkv in (1, 149):                            # a list split over a cluster, and one CTA a list
+        k, v = (_rand((1, n, hkv, d), 520 + i, torch.float32) for i in range(2))
+        v = v.clamp(-4, 4) * (100.0 if fmt == "e4m3" else 24.0) * 2.0 ** exponent
+        q = _rand((1, lq, group * hkv, d), 530, dtype)
+        idx, cnt = _lists([n - lq], 1, 0, n, 1, 1)
+        for layout in ("behind", "ahead", "tiles", "blocks", "one", "first") if hkv == 1 else ("behind", "ahead", "blocks"):
+            cache = _cache(1, n, hkv, d, fmt, block)
+            x = torch.where(_loud_keys(layout, n, block)[None, :, None, None], v, 0.0)
+            qas.cache_write_q8(cache, k.to(DEV), x.to(DEV), 0)
+            s = cache.v_scale.cpu()
+            assert 2.0 ** (exponent - 2) <= s.max() <= 2.0 ** exponent and s.min() == 2.0 ** -100
+            kv, vv = (y.cpu().double().numpy() for y in qas.cache_read_q8(cache, dtype=torch.float32))
+            o, lse = qas.sparse_attn_q8(q.to(DEV), cache, n - lq, idx.to(DEV), cnt.to(DEV), p, want_lse=True)
+            _check(o, lse, _reference(q, kv, vv, [n - lq], idx, cnt, 0, n), dtype, d)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 128)])
+def test_attention_nan_scale_of_a_block_that_a_query_does_not_attend(fmt, dtype, d):
+    """Drafted tokens on both sides of a block's start: a NaN scale behind it is no matter of
+    the queries ahead of it."""
+    n, hkv, block, c0 = 320, 2, 32, 317 - 32         # queries at 285 .. 289: the last two in the block from 288
+    cache, _, _ = _filled(1, n, hkv, d, fmt, block, [n], 541)
+    q = _rand((1, 5, 8, d), 542, dtype).to(DEV)
+    idx, cnt = _lists([c0], 1, 16, 64, 40, 543, short=False)
+    args = (c0, idx.to(DEV), cnt.to(DEV), qas.params(16, 64, 40, 0))
+    good, good_lse = qas.sparse_attn_q8(q, cache, *args, want_lse=True)
+    for scale in (cache.k_scale, cache.v_scale):
+        was = scale[0, 9, 1].clone()
+        scale[0, 9, 1] = float("nan")
+        o, lse = qas.sparse_attn_q8(q, cache, *args, want_lse=True)
+        assert o[0, 3:, 4:].isnan().all() and lse[0, 3:, 4:].isnan().all()
+        assert torch.equal(o[0, :3], good[0, :3]) and torch.equal(lse[0, :3], good_lse[0, :3])
+        assert torch.equal(o[0, :, :4], good[0, :, :4])
+        scale[0, 9, 1] = was
+    qas.device_status()
+
+
 def test_offsets_past_32_bits():
     # 3 sequences of 1M rows of 1 KB: the last ones lie past 2^31 bytes of each operand
     b, n_cap, hq, hkv, d, block = 3, 1 << 20, 32, 8, 128, 64
