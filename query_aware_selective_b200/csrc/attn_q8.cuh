@@ -185,11 +185,11 @@ __device__ __forceinline__ int q8_query_exp(float amax) {
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, float* f) {
   if constexpr (sizeof(T) == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     const float2 a = bf16x2_to_float2(v.x), b = bf16x2_to_float2(v.y);
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
   } else {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 v = *reinterpret_cast<const float4*>(p);
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
   }
 }
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
   // at once would wait for a load that may miss all the way to HBM.
   constexpr int kAhead = 2;
   auto at = [&](int s) { return min(s * kQ8Keys + (lane & 15), n_keys - 1); };
-  auto entry = [&](int s) -> int32_t { return __ldg(ib + min(max(at(s) - ni, 0), (int)kl.idx_stride - 1)); };
+  auto entry = [&](int s) -> int32_t { return ib[min(max(at(s) - ni, 0), (int)kl.idx_stride - 1)]; };
   const uint32_t ring = smem_u32(q8sm) + warp * (kQ8Stages * q8_stage_bytes<D>());
   auto issue = [&](int pos, uint32_t st) {
 #pragma unroll

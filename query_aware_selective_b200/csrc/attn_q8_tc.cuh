@@ -276,7 +276,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
 #pragma unroll
     for (int u = 0; u < NST; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) raw[u][h] = __ldg(entry(u, prow + 32 * h));
+      for (int h = 0; h < 2; ++h) raw[u][h] = *entry(u, prow + 32 * h);
   }
   // queries: thread (r, part) of the first tile group takes DPT dims of row r, loaded now for
   // the time that the list's length and the setup take
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
     const uint2* qp = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) +
         (((int64_t)b * a.lq + i) * a.hq + g * a.G + hl) * 128 + q_part * DPT);
 #pragma unroll
-    for (int e = 0; e < DPT / 4; ++e) q_raw[e] = __ldg(qp + e);
+    for (int e = 0; e < DPT / 4; ++e) q_raw[e] = qp[e];
   }
   const int32_t n_listed = kl.count[list];
   if (threadIdx.x == 0) {

@@ -22,6 +22,10 @@ namespace esa {
 // Programmatic dependent launch: a kernel launched with the attribute may be set up while
 // the one before it in the stream still drains; nothing of global memory may be touched
 // before this wait, which returns once that kernel is complete and its writes are visible.
+// What a kernel before may have written (rows, codes, scales, lists, queries) is then read by
+// plain loads: the read-only path (ld.global.nc, __ldg) is for data that nothing writes in the
+// kernel's whole lifetime, which begins under the writer, and the compiler may lift such a
+// load above the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 constexpr int kQ8E4M3 = 0, kQ8Int8 = 1;
@@ -122,14 +126,21 @@ __device__ __forceinline__ bool q8_write_range(const CacheWriteArgs& a, int b, i
   return true;
 }
 
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 // 32 bytes of global memory in one load (they are 32-byte aligned), or in two
 __device__ __forceinline__ void ld_global_32(const void* p, bool wide, uint32_t* w) {
   if (wide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(p));
   } else {
-    const uint4 a = ld_stream16(p), b = ld_stream16(static_cast<const uint8_t*>(p) + 16);
+    const uint4 a = ld_once16(p), b = ld_once16(static_cast<const uint8_t*>(p) + 16);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
@@ -302,10 +313,10 @@ __device__ __forceinline__ void q8_widen_store(const uint32_t* c, float s, T* ds
 template <int BYTES>
 __device__ __forceinline__ void q8_load_codes(const uint8_t* p, uint32_t* c) {
   if constexpr (BYTES == 16) {
-    const uint4 v = ld_stream16(p);
+    const uint4 v = ld_once16(p);
     c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
   } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     c[0] = v.x; c[1] = v.y;
   }
 }
@@ -348,7 +359,7 @@ __device__ __forceinline__ void q8_move(const uint8_t* codes, const float* scale
     // behind its own load)
     const uint32_t at = max(pos[u], 0);
     q8_load_codes<N>(codes + (uint64_t)at * row_bytes, c[u]);
-    s[u] = __ldg(scale + (uint64_t)(at >> bshift) * (uint32_t)hkv);
+    s[u] = scale[(uint64_t)(at >> bshift) * (uint32_t)hkv];
   }
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const Cache
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
     const int64_t r = row0 + u * tile.rows;
-    pos[u] = r < a.n ? (a.idx ? __ldg(a.idx + (int64_t)b * a.n + r) : (int)(a.start + r)) : -1;
+    pos[u] = r < a.n ? (a.idx ? a.idx[(int64_t)b * a.n + r] : (int)(a.start + r)) : -1;
   }
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) pos[u] = pos[u] < a.n_cap ? pos[u] : -1;

@@ -2,6 +2,8 @@
 refused before anything is launched, by the C ABI and by the binding."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -139,3 +141,14 @@ def test_binding_refuses_cpu_tensors():
         qas.CacheQ8(k, s, k.clone(), s.clone(), 16)
     with pytest.raises(ValueError, match="CUDA"):
         qas.cache_q8(1, 64, 2, 64, device="cpu")
+
+
+def test_kernels_set_up_under_their_producer_read_by_plain_loads():
+    """The 8-bit cache's kernels start under the kernel before them and read what it wrote: no
+    load of theirs takes the read-only path."""
+    csrc = os.path.join(os.path.dirname(qbuild.__file__), "csrc")
+    for name in ("cache_q8.cuh", "attn_q8.cuh", "attn_q8_tc.cuh", "keylist.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert "pdl_wait()" in code or name == "keylist.cuh"
+        assert not re.search(r"__ldg|\.nc\b|ld_stream16|__restrict__", code), name
