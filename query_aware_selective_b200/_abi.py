@@ -666,7 +666,7 @@ def sparse_attn_q8(q: torch.Tensor, cache: CacheQ8, c0: int, idx: torch.Tensor, 
     b, lq, hq, d = q.shape
     dt = _q8_dtype(q)
     wp, wn = None, 0
-    if lq > 1:                 # a single query needs no workspace
+    if lq > 1 or hq > 32 * cache._shape[1]:    # a single query of up to 32 heads a KV head needs no workspace
         if workspace is not None and workspace.get_device() != cache._dev:
             raise ValueError("the workspace must be on the cache's device")
         ws = _workspace(sparse_attn_q8_workspace_size(b, lq, c0, hq, cache._shape[1], d, dt, p), q.device, workspace)

@@ -1,6 +1,7 @@
 """Host-side checks of the 8-bit cache calls that need no GPU: every bad argument is
 refused before anything is launched, by the C ABI and by the binding."""
 import ctypes
+import itertools
 import math
 import os
 import re
@@ -152,3 +153,32 @@ def test_kernels_set_up_under_their_producer_read_by_plain_loads():
             code = re.sub(r"//[^\n]*", "", f.read())
         assert "pdl_wait()" in code or name == "keylist.cuh"
         assert not re.search(r"__ldg|\.nc\b|ld_stream16|__restrict__", code), name
+
+
+def _cpu_cache(b, n_cap, hkv, d):
+    """A CacheQ8 on the host, for calls that are stopped before the library."""
+    c = object.__new__(qas.CacheQ8)
+    c._k = c._v = torch.zeros((b, n_cap, hkv, d), dtype=torch.int8)
+    c._k_scale = c._v_scale = torch.zeros((b, n_cap // 16, hkv))
+    c._c = _abi.EsaCacheQ8(FAKE, FAKE, FAKE, FAKE, n_cap, b, hkv, d, 16, 1)
+    c._dev, c._shape = -1, (b, hkv, d)
+    return c
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_binding_brings_the_workspace_that_a_call_asks_for(lib, monkeypatch, d, dtype):
+    seen = {}
+    monkeypatch.setattr(_abi, "_q8_call", lambda cache, where, *args: seen.update(ws=args[-2], size=args[-1]))
+    p = _abi.params(16, 32, 24, 2)
+    asked = set()
+    for b, hkv, group, lq in itertools.product((1, 25, 64, 80), (1, 2, 8), (1, 5, 16, 24, 32, 33, 48, 49, 64, 128, 160),
+                                               (1, 2, 5)):
+        need = _abi.sparse_attn_q8_workspace_size(b, lq, 100, group * hkv, hkv, d, int(dtype == torch.bfloat16), p)
+        q = torch.empty((b, lq, group * hkv, d), dtype=dtype)
+        qas.sparse_attn_q8(q, _cpu_cache(b, 128, hkv, d), 100, torch.zeros((b, 24), dtype=torch.int32),
+                           torch.zeros(b, dtype=torch.int32), p)
+        assert seen["size"] >= need and (need == 0 or seen["ws"] % 256 == 0), (b, hkv, group, lq)
+        if need:
+            asked.add(lq)
+    assert asked == ({1, 2, 5} if dtype == torch.bfloat16 else set())

@@ -490,6 +490,25 @@ def test_attention_chunk_any_group_and_heads_of_64(fmt, chunk, b, lq, n_cap, hq,
     assert (guard[:128] == 7).all() and (guard[-128:] == 7).all()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("b,hq,hkv,d,lists", [(80, 64, 1, 128, 1), (80, 64, 1, 64, 1), (25, 128, 1, 128, 1),
+                                              (25, 192, 2, 128, 2), (14, 256, 1, 128, 1), (40, 128, 2, 64, 2)])
+def test_attention_single_queries_of_many_heads_on_one(fmt, b, hq, hkv, d, lists):
+    """One query a sequence, but so many rows a KV head that the call takes the chunk form."""
+    n_cap, n_init, window, topk = 300, 16, 64, 50
+    c0 = n_cap - 4
+    cache, kv, vv = _filled(b, n_cap, hkv, d, fmt, 32, [c0 + 1] * b, 137)
+    q = _rand((b, 1, hq, d), 147, torch.bfloat16)
+    idx, cnt = _lists([c0] * b, lists, n_init, window, topk, 157)
+    p = qas.params(n_init, window, topk, 2, 10.0)
+    assert qas._abi.sparse_attn_q8_workspace_size(b, 1, c0, hq, hkv, d, 1, p) > 0
+    guard = torch.full((b * hq * d + 256,), 7.0, dtype=torch.bfloat16, device=DEV)
+    o, lse = qas.sparse_attn_q8(q.to(DEV), cache, c0, idx.to(DEV), cnt.to(DEV), p, want_lse=True,
+                                out=guard[128:-128].view(b, 1, hq, d))
+    _check(o, lse, _reference(q, kv, vv, [c0] * b, idx, cnt, n_init, window), torch.bfloat16, d, chunk=True)
+    assert (guard[:128] == 7).all() and (guard[-128:] == 7).all()
+
+
 @pytest.mark.parametrize("hq,hkv,d,lq", [(10, 2, 128, 210), (28, 4, 64, 140)])
 def test_attention_chunk_nan_and_infinity_stay_in_their_rows(hq, hkv, d, lq):
     """A query row with a NaN or an infinity, beside rows of another head and of another query."""
@@ -999,6 +1018,24 @@ def test_prefill_over_a_cache_of_heads_of_64(dtype, hq, hkv, chunk):
         assert (ws > 0) == (dtype == torch.bfloat16)
         _check(out[:, c0:c0 + lq], None, _reference(q[:, c0:c0 + lq], kv, vv, [c0] * b, idx, cnt, n_init, window), dtype,
                d, chunk=ws > 0)
+
+
+def test_prefill_whose_last_chunk_is_one_row_of_many_heads():
+    b, n, chunk, hq, hkv, d, dc, n_init, window, topk = 50, 65, 32, 64, 1, 128, 128, 4, 16, 12
+    g = torch.Generator().manual_seed(16)
+    q, k, v = (torch.randn((b, n, h, d), generator=g).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    wq, wk = (torch.randn((hq * d, dc), generator=g).to(DEV) / 64 for _ in range(2))
+    p = qas.params(n_init, window, topk, 2, 45.25)
+    cache = _cache(b, n, hkv, d, "int8", 16)
+    pf = pipeline.EsaPrefill(b, n, chunk, hq, hkv, d, dc, p, cache=cache)
+    assert [lq for _, lq in pf.chunks()][-1] == 1
+    out = pf.run(q.to(DEV), k.to(DEV), v.to(DEV), wq, wk)
+    kv, vv = _values(cache)
+    for ci, (c0, lq) in enumerate(pf.chunks()):
+        idx, cnt = pf.idx_all[ci].cpu().view(b, 1, topk), pf.count_all[ci].cpu().view(b, 1)
+        assert qas._abi.sparse_attn_q8_workspace_size(b, lq, c0, hq, hkv, d, 1, p) > 0
+        _check(out[:, c0:c0 + lq], None, _reference(q[:, c0:c0 + lq], kv, vv, [c0] * b, idx, cnt, n_init, window),
+               torch.bfloat16, d, chunk=True)
 
 
 def test_captured_behind_copies_and_joined_streams():
