@@ -507,7 +507,10 @@ def cache_q8(batch: int, n_cap: int, hkv: int, head_dim: int, dtype: torch.dtype
 # (The helpers below are written for few interpreter steps: a call on a small batch takes
 # longer here than on the GPU.)
 _DTYPE_CODES = {torch.float32: ESA_F32, torch.bfloat16: ESA_BF16}
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (torch's own entries take a third of the public calls' time; a torch without them, one built
+# for the CPU among others, has the public calls)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _q8_call(cache: CacheQ8, where: str, *args):

@@ -5,6 +5,8 @@ import itertools
 import math
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -182,3 +184,15 @@ def test_binding_brings_the_workspace_that_a_call_asks_for(lib, monkeypatch, d, 
         if need:
             asked.add(lq)
     assert asked == ({1, 2, 5} if dtype == torch.bfloat16 else set())
+
+
+def test_import_needs_no_private_name_of_torch():
+    code = ("import torch\n"
+            "for name in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    delattr(torch._C, name)\n"
+            "import query_aware_selective_b200 as qas\n"
+            "from query_aware_selective_b200 import _abi, cost, pipeline, synthetic\n"
+            "assert _abi._current_device is torch.cuda.current_device and callable(_abi._raw_stream)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(qas.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

@@ -855,6 +855,24 @@ def test_captured_step_replays_with_new_lengths():
     qas.device_status()
 
 
+def test_calls_by_torchs_public_entries(monkeypatch):
+    """A torch without the private entries that the binding prefers: the same device and stream."""
+    want = _step(_step_state([300, 299])).clone()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    seen = []
+    monkeypatch.setattr(qas._abi, "_current_device", torch.cuda.current_device)
+    monkeypatch.setattr(qas._abi, "_raw_stream",
+                        lambda dev: seen.append(torch.cuda.current_stream(dev).cuda_stream) or seen[-1])
+    s = _step_state([300, 299])
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = _step(s)
+        assert torch.cuda.current_stream().cuda_stream == stream.cuda_stream == seen[-1]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_two_graphs_and_two_streams_at_once():
     states = [_step_state([300 + i, 200 + i]) for i in range(4)]
     want = [_step(_step_state([300 + i, 200 + i])).clone() for i in range(4)]
