@@ -544,8 +544,9 @@ const char* esa_last_error(void);
  * device. Returns ESA_OK, ESA_ERR_TIMEOUT if a kernel's bounded wait ran out since the
  * last read (the message names the kernel and the wait), ESA_ERR_CUDA if a kernel
  * stopped early on a launch-environment check (e.g. misaligned shared memory), or
- * ESA_ERR_INVALID_ARG if a variable-length call read a length outside [1, n_cap] or a
- * write to an 8-bit cache read a NaN or an infinity. */
+ * ESA_ERR_INVALID_ARG if a variable-length call read a length outside [1, n_cap] (it went
+ * on with the nearest one inside), if a write to an 8-bit cache got lengths that do not fit
+ * (it left that sequence as it was) or read a NaN or an infinity. */
 esa_status_t esa_device_status(void* stream);
 
 /* esa_wait_selftest - runs the bounded-wait path on demand: one CTA waits on a barrier

@@ -119,7 +119,7 @@ __device__ __forceinline__ bool q8_write_range(const CacheWriteArgs& a, int b, i
   end = a.seq_len[b];
   if (t == 0) return false;
   if (t < 0 || t > a.rows || end < t || end > a.n_cap) {
-    if (threadIdx.x == 0) record_status(1u, 705);
+    if (threadIdx.x == 0) record_status(8u, 705);
     return false;
   }
   start = end - t;

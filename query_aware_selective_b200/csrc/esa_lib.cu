@@ -408,6 +408,11 @@ esa_status_t esa_device_status(void* stream) {
   if (code == 5u) return fail(ESA_ERR_CUDA, "kernel site %u found its shared memory misaligned and stopped", site);
   if (code == 1u)
     return fail(ESA_ERR_INVALID_ARG, "kernel site %u read a sequence length outside [1, n_cap] (clamped)", site);
+  if (code == 8u)
+    return fail(ESA_ERR_INVALID_ARG,
+                "kernel site %u: a write to an 8-bit cache got lengths that do not fit (new rows outside [0, rows], or "
+                "a length outside [new rows, n_cap]); the sequence was left as it was",
+                site);
   if (code == 7u)
     return fail(ESA_ERR_INVALID_ARG, "kernel site %u wrote NaN or infinite values to an 8-bit cache", site);
   if (code == 6u)

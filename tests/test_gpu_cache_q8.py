@@ -206,6 +206,27 @@ def test_write_varlen_lengths_that_do_not_fit():
     assert cache.k_scale[:3].isnan().all() and cache.k_scale[3, 0].isfinite().all()
 
 
+def test_a_write_that_does_not_fit_is_reported_as_one():
+    """Not as a length that was clamped: nothing of the sequence was written."""
+    cache = _cache(2, 64, 1, 64, "int8", 16)
+    k = _rand((2, 8, 1, 64), 1, torch.bfloat16).to(DEV)
+    good = torch.tensor([8, 8], device=DEV)
+    for ends, new in (([65, 8], None), ([7, 8], None), ([8, 8], [9, 8]), ([8, 8], [-1, 8])):
+        qas.cache_write_q8_varlen(cache, k, k, torch.tensor(ends, device=DEV),
+                                  good if new is None else torch.tensor(new, device=DEV))
+        with pytest.raises(qas.EsaError, match="left as it was") as e:
+            qas.device_status()
+        assert "clamped" not in str(e.value) and e.value.status == qas._abi.ESA_ERR_INVALID_ARG
+        assert (cache.k[0].view(torch.uint8) == 0x7f).all() and cache.k_scale[0].isnan().all()
+        qas.device_status()                        # reported once
+    q = _rand((2, 1, 1, 64), 2, torch.bfloat16).to(DEV)
+    cache = qas.cache_q8(2, 64, 1, 64, torch.int8, 16, device=DEV)
+    zero = torch.zeros((2, 4), dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    qas.sparse_attn_q8_varlen(q, cache, torch.tensor([65, 8], device=DEV), *zero, qas.params(4, 8, 4, 0))
+    with pytest.raises(qas.EsaError, match="clamped"):
+        qas.device_status()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_write_of_nan_and_infinity(fmt, dtype):
