@@ -378,15 +378,17 @@ __device__ __forceinline__ void q8_move(const uint8_t* codes, const float* scale
 
 // Row (b, r) of the result is cache row start + r, or idx[b, r] (zeros where that is not a
 // row of the cache). A thread makes 32 bytes of the result from 16 (8) codes, kReadPer
-// rows with their loads in flight together (2, 4, 8 rows: 48, 37.6, 41.7 us for 32000 rows
-// of 8 heads of 128). Bound by HBM, two thirds of it writes: 197 MB in 37.6 us, 5.23 TB/s;
-// a device copy of 262 MB takes 45.5 us (5.76 TB/s) and a fill of 131 MB 24.9 us (5.26).
+// rows with their loads in flight together (2, 4, 8 rows: 7.7, 7.4, 8.3 us for 8192 listed
+// rows of 8 heads of 128, 31.1, 31.1, 31.3 for 32000 consecutive ones). Bound by HBM, two
+// thirds of it writes: 197 MB in 30.9 us, 6.36 TB/s; to fp32 328 MB in 50.2 us, 6.53 TB/s (a
+// device copy of 262 MB: 41.6 us, 6.30 TB/s).
 // grid (row tiles * column CTAs, B, operands).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const CacheReadArgs a) {
   constexpr int N = 32 / sizeof(T);
   const int op = blockIdx.z, b = blockIdx.y;
-  T* out = static_cast<T*>(a.out[op]);
+  // (indexed by op, the arguments would be copied to local memory)
+  T* out = static_cast<T*>(op ? a.out[1] : a.out[0]);
   if (!out) return;
   const uint32_t row_bytes = (uint32_t)(a.hkv * a.d);
   const ReadTile tile(row_bytes / N);
@@ -403,8 +405,8 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const Cache
   }
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) pos[u] = pos[u] < a.n_cap ? pos[u] : -1;
-  q8_move<T, FMT>(a.codes[op] + (int64_t)b * a.n_cap * row_bytes + col * N,
-                  a.scale[op] + (int64_t)b * a.nblk * a.hkv + col * N / a.d, row_bytes, a.hkv, a.bshift, pos,
+  q8_move<T, FMT>((op ? a.codes[1] : a.codes[0]) + (int64_t)b * a.n_cap * row_bytes + col * N,
+                  (op ? a.scale[1] : a.scale[0]) + (int64_t)b * a.nblk * a.hkv + col * N / a.d, row_bytes, a.hkv, a.bshift, pos,
                   out + (int64_t)b * a.n * row_bytes + col * N, row0, tile.rows, a.n);
 }
 
