@@ -1300,6 +1300,8 @@ int q8_box_group(int g) { return std::min(g & -g, esa::kTcRows); }
 // against 171 for 128 (sequence, KV head)s of 40. Heads of 64: attn_q8_kernel takes 16 rows a
 // unit, 62 us for 224 units against 70 staged, 92 for 416 against 71, 220 for 1024 against
 // 68, and with 128 (sequence, KV head)s 69 us for 20 rows against 109, 133 for 52 against 109.
+// (148 units: the SMs of a B200. It is no property of the current device, because the size of the
+// workspace is asked for without one; with other counts the rule only splits elsewhere.)
 bool q8_chunk_form(int64_t batch, int32_t lq, int32_t hq, int32_t hkv, int32_t head_dim, esa_dtype_t dt) {
   const int g = hq / hkv;
   const int64_t rows = (int64_t)lq * g, n = batch * hkv;
@@ -1322,14 +1324,19 @@ int64_t q8_staged_rows(int32_t lq, int64_t c0, const esa_params_t& p) {
 // which left 8 CTAs to a second wave, 44 against 25 when one wave took that); 88 units in 2
 // waves of clusters of 3 take 57 us, 68 without clusters; 152 in 3 waves of 2 70, 74 in 2
 // waves without; 512 in 4 waves 153, 164 in 7 of 2 (without the tenth). How many fit at once
-// is asked once per kernel and context (a byte each: CTAs an SM, clusters of 2 .. 8).
+// is asked once per kernel and context.
 template <typename Kernel>
 esa_status_t q8_cluster_size(Kernel kernel, int threads, int smem, int64_t units, int64_t n_keys, int64_t most,
                              int* csize) {
+  // what fits at once of clusters of 1, 2 .. 8 CTAs: a field each, its last bit that of the next
+  // one's first
+  static constexpr int first[9] = {0, 16, 24, 32, 40, 46, 52, 58, 64};
+  auto field = [](int c) { return ((uint64_t)1 << (first[c] - first[c - 1])) - 1; };
   intptr_t fit = 0;
   const esa_status_t st = per_context(reinterpret_cast<const void*>(kernel), &fit, [&](intptr_t* v) {
     ESA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    for (int c = 2; c <= 8; ++c) {
+    uint64_t all = 0;
+    for (int c = 1; c <= 8; ++c) {
       cudaLaunchConfig_t q = {};
       q.gridDim = dim3(c);
       q.blockDim = dim3(threads);
@@ -1343,18 +1350,16 @@ esa_status_t q8_cluster_size(Kernel kernel, int threads, int smem, int64_t units
       q.numAttrs = 1;
       int n = 0;
       ESA_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &q));
-      *v |= (intptr_t)std::min(n, 255) << (8 * (c - 1));
+      all |= std::min((uint64_t)n, field(c)) << first[c - 1];
     }
-    int per_sm = 0;
-    ESA_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem));
-    *v |= per_sm;
+    *v = (intptr_t)all;
     return ESA_OK;
   });
   if (st != ESA_OK) return st;
   *csize = 1;
   double least = 0;
   for (int c = 1; c <= 8 && (c == 1 || c <= most); ++c) {
-    const int64_t at_once = c == 1 ? (fit & 255) * 148 : (fit >> (8 * (c - 1))) & 255;
+    const int64_t at_once = (int64_t)((uint64_t)fit >> first[c - 1] & field(c));
     if (at_once == 0) continue;
     const int64_t waves = cdiv(units, at_once);
     const double cost = (double)waves * (1024 + (double)n_keys / c);
