@@ -399,8 +399,9 @@ size_t esa_sparse_attn_varlen_workspace_size(int32_t batch, int64_t n_cap, int32
  *   format:           ESA_Q8_E4M3 (4 exponent and 3 mantissa bits, +-448) or
  *                     ESA_Q8_INT8 (-127 .. 127)
  *   block:            16, 32, 64 or 128;  head_dim: 64 or 128;  n_cap < 2^31
- * All buffers are the caller's, k and v (and their scales) different ones; nothing needs to be initialised before the first write of
- * a sequence at position 0 (or at any multiple of block). */
+ * All buffers are the caller's, k and v (and their scales) different ones; nothing needs to be
+ * initialised before the first write of a sequence at position 0 (or at any multiple of
+ * block). */
 typedef enum { ESA_Q8_E4M3 = 0, ESA_Q8_INT8 = 1 } esa_q8_format_t;
 
 typedef struct {
@@ -461,14 +462,24 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  *   idx, count: [batch, lists, p.topk] and [batch, lists] int32, as the selections write them
  *   lse:        NULL or [batch, lq, hq] fp32
  * Scales of keys may be any positive numbers below 2^121, those of values below 2^98 (under
- * 2^-100, or zero, they count as 2^-100), and the codes of attended keys any but e4m3's NaN (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a
- * row of NaN. hq is a multiple of hkv; no limit on their ratio. Entries of idx may repeat
- * (count may be up to topk whatever the length of the middle); entries outside the cache are
- * clamped into it. Codes are exact in the products; softmax weights keep 11 bits or more (22
- * for fp32), and 2^-26 of the largest at least. A large chunk of bf16
- * queries dequantises its keys and values into the workspace as bf16 (exact for scales that
- * are powers of two) and rounds its weights to bf16. The workspace is for that
- * alone: ask esa_sparse_attn_q8_workspace_size (256-byte aligned; 0 bytes for other calls).
+ * 2^-100, or zero, they count as 2^-100), and the codes of attended keys any but e4m3's NaN
+ * (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a row of NaN.
+ * hq is a multiple of hkv; no limit on their ratio. Entries of idx may repeat (count may be up
+ * to topk whatever the length of the middle); entries outside the cache are clamped into it.
+ * Precision. Sums are fp32 or exact. Which rounding the queries and the softmax weights get
+ * goes by dtype, head_dim, format and the number of query rows (a weight here is that of a key
+ * times the scale of its value):
+ *   bf16, head_dim 128: codes exact; an element of a query to 2^-21 (e4m3) or 2^-20 (int8) of
+ *     its row's largest, so that bf16's own 8 bits are whole down to 2^-12 of it; weights to
+ *     2^-13 of themselves and 2^-26 of the largest of 128 keys (e4m3), to 2^-28 of that (int8)
+ *   bf16, head_dim 64: codes exact; queries exact down to 2^-30 of the row's largest; weights to
+ *     2^-11 of themselves and 2^-35 of the largest
+ *   fp32: codes exact; queries and weights to 2^-21 of themselves (the ends as above)
+ *   a large chunk of bf16 queries (a call whose esa_sparse_attn_q8_workspace_size is not 0): the
+ *     listed keys and values go into the workspace as bf16 (exact for scales that are powers of
+ *     two), queries are exact, weights are rounded to bf16 (2^-8), as in esa_sparse_attn
+ * The workspace is for that last form alone (256-byte aligned; other calls need none, and a
+ * single query needs it too when there are enough heads on a KV head).
  * ESA_ERR_UNSUPPORTED for more than 65535 row tiles (hkv * ceil(lq * hq / hkv / 16), / 8 with
  * up to 8 rows; 24 for bf16 with head_dim 128). Other errors as for esa_sparse_attn. */
 esa_status_t esa_sparse_attn_q8(const void* q, esa_dtype_t dt, esa_cache_q8_t cache, int32_t lq, int64_t c0,

@@ -12,6 +12,8 @@
 //         query, three for a weight (relative 2^-13)
 //   int8: digits of 7 bits of an integer: three for a query (its row's largest is 2^19 to
 //         2^20), four for a weight (its tile's largest is 2^27)
+// (a query's element to 2^-21 or 2^-20 of its row's largest: bf16's 8 bits are whole down to
+// 2^-12 of that, and one more piece would be a column to load and to add for each key and row)
 // and a row's value is the sum of its columns times 2^(-4 p) or 2^(-7 p). Column (rg NW + p)
 // WR + r is piece p of row r of row group rg.
 // Weights are taken relative to their key tile's own maximum (of 128 keys), and a tile's O

@@ -655,6 +655,106 @@ def test_attention_scales_far_apart():
         _check(o, lse, _reference(qd, kv, vv, [n_cap - 1], idx, cnt, 0, n_cap), dtype, d)
 
 
+# What the kernels on the codes promise of a weight and of a query, by (dtype, head dim, format):
+# u, the relative rounding of a weight: 2^-13 for three e4m3 pieces of 4 significant bits, none
+#    for int8 digits, 2^-11 for an f16, 2^-21 for two (fp32 queries);
+# f, its absolute rounding in units of its tile's largest: 2^-26, 2^-28, and 2^-35 for f16;
+# e, the rounding of a query element in units of its row's largest: two e4m3 pieces end at steps
+#    of 2^-9 16^-1 for a largest of 2^7 or more, so half of 2^-13 in 2^7: 2^-21; three digits
+#    round to a whole number with a largest of 2^19 or more: 2^-20; an f16 has steps of 2^-24
+#    for a largest of 2^13 or more: 2^-38, and no relative rounding of a bf16.
+PROMISED = {(torch.bfloat16, 128, "e4m3"): (2.0 ** -13, 2.0 ** -26, 2.0 ** -21),
+            (torch.bfloat16, 128, "int8"): (0.0, 2.0 ** -28, 2.0 ** -20),
+            (torch.bfloat16, 64, "e4m3"): (2.0 ** -11, 2.0 ** -35, 2.0 ** -38),
+            (torch.bfloat16, 64, "int8"): (2.0 ** -11, 2.0 ** -35, 2.0 ** -38),
+            (torch.float32, 128, "e4m3"): (2.0 ** -21, 2.0 ** -35, 2.0 ** -38),
+            (torch.float32, 64, "int8"): (2.0 ** -21, 2.0 ** -35, 2.0 ** -38)}
+
+
+def _cancelling(b, hkv, d, group, dtype, fmt):
+    """Four keys, all logits along dim 0 (for a query of 1 about -0.3, -2.7 and -5.5 under the
+    first's), and values that cancel under the weights of each KV head's first query, each key
+    finer than the one before. Returns q, k, v; the cache holds v as it is."""
+    g = torch.Generator().manual_seed(17)
+    n = 4
+    k = torch.zeros((b, n, hkv, d))
+    k[..., 0] = torch.tensor([0.0, -3.0, -30.0, -60.0])[None, :, None]
+    q = torch.zeros((b, 1, group * hkv, d))
+    q[..., 0] = (1.0 + torch.rand((b, 1, group * hkv), generator=g) / 4) * (d ** 0.5 / 11)
+    q = q.to(dtype)
+    unit = 0.5 if fmt == "e4m3" else 1.0                    # the scale of a block whose largest value is 120
+    held = torch.from_numpy(oc.numbers(fmt)) * unit
+    held = held[held <= 120]
+    both = torch.cat([-held.flip(0), held])
+    v = torch.zeros((b, n, hkv, d), dtype=torch.float64)
+    some = held[held >= 60]
+    v[:, 0] = some[torch.randint(len(some), (b, hkv, d), generator=g)]
+    v[:, 0, :, 0] = 120.0
+    x = torch.einsum("bnh,bh->bnh", k[..., 0].double(), q[:, 0, ::group, 0].double()) * d ** -0.5
+    p = x.softmax(dim=1)
+    rest = p[:, 0, :, None] * v[:, 0]
+    for j in range(1, n):
+        want = -rest / p[:, j, :, None]
+        v[:, j] = both[(want[..., None] - both).abs().argmin(dim=-1)]
+        rest = rest + p[:, j, :, None] * v[:, j]
+    return q, k, v.float()
+
+
+@pytest.mark.parametrize("group", [1, 6, 12])
+@pytest.mark.parametrize("dtype,d,fmt", list(PROMISED))
+def test_attention_weights_keep_their_bits(dtype, d, fmt, group):
+    """What is left of an output dim is far below its values, and shows the rounding of single
+    weights."""
+    b, n, hkv = 16, 4, 2
+    q, k, v = _cancelling(b, hkv, d, group, dtype, fmt)
+    cache = qas.cache_q8(b, 16, hkv, d, DTYPE[fmt], 16, device=DEV)
+    qas.cache_write_q8(cache, k.to(DEV), v.to(DEV), 0)
+    kv, vv = (y.cpu().double().numpy() for y in qas.cache_read_q8(cache, dtype=torch.float32))
+    assert np.array_equal(kv[:, :n], k.double().numpy()) and np.array_equal(vv[:, :n], v.double().numpy())
+    idx, cnt = torch.zeros((b, 1, 1), dtype=torch.int32), torch.zeros((b, 1), dtype=torch.int32)
+    p = qas.params(0, n, 1, 0)
+    o, _ = qas.sparse_attn_q8(q.to(DEV), cache, n - 1, idx.to(DEV), cnt.to(DEV), p)
+    qas.device_status()
+    ref_o, _, big, xmax, least = _reference(q, kv, vv, [n - 1] * b, idx, cnt, 0, n)
+    u, f, e = PROMISED[dtype, d, fmt]
+    dx = xmax[..., None] * (8 * 2.0 ** -24 + e)              # one product a logit, its scalings, the query's rounding
+    bound = torch.finfo(dtype).eps / 2 * np.abs(ref_o) + big * (u + 2 * dx + 2.0 ** -19) + f * least
+    # (of each KV head's first query the rounding of the output leaves room to see a weight's)
+    assert np.median((bound / big)[:, :, ::group]) < 2.0 ** (-10 if u else -14)
+    worst = float((np.abs(o.cpu().double().numpy() - ref_o) / bound).max())
+    assert worst <= 1.0, f"{worst} times the bound"
+
+
+@pytest.mark.parametrize("more", [6, 10, 13, 16])
+@pytest.mark.parametrize("dtype,d,fmt", list(PROMISED))
+def test_attention_queries_with_a_loud_channel(dtype, d, fmt, more):
+    """One channel of the queries 2^more above the others, where the keys hold nothing: the logits
+    are ordinary, and of the other channels a query keeps what its format leaves."""
+    n_cap, hq, hkv, lq = 400, 8, 2, 3
+    k, v = (_rand((1, n_cap, hkv, d), 620 + i, torch.float32) for i in range(2))
+    q = _rand((1, lq, hq, d), 630, torch.float32)
+    q[..., 5] = 2.0 ** more * (1.0 + q[..., 5].abs() / 4) * q[..., 6].sign()
+    k[..., 5] = 0.0
+    q = q.to(dtype)
+    cache = _cache(1, n_cap, hkv, d, fmt, 32)
+    qas.cache_write_q8(cache, k.to(DEV), v.to(DEV), 0)
+    kv, vv = (y.cpu().double().numpy() for y in qas.cache_read_q8(cache, dtype=torch.float32))
+    c0 = n_cap - lq
+    idx, cnt = _lists([c0], 1, 0, n_cap, 1, 1)
+    p = qas.params(0, n_cap, 1, 0)
+    o, lse = qas.sparse_attn_q8(q.to(DEV), cache, c0, idx.to(DEV), cnt.to(DEV), p, want_lse=True)
+    qas.device_status()
+    ref_o, ref_lse, big, xmax, least = _reference(q, kv, vv, [c0], idx, cnt, 0, n_cap)
+    u, f, e = PROMISED[dtype, d, fmt]
+    loud = q.double().abs().amax(dim=-1).numpy() * d ** -0.5 * float(np.abs(kv).sum(axis=-1).max())
+    dx = xmax * (d + 8) * 2.0 ** -24 * (2 if dtype == torch.float32 else 1) + e * loud
+    bound = torch.finfo(dtype).eps / 2 * np.abs(ref_o) + \
+        big * (u + np.expm1(2 * dx[..., None]) + 2.0 ** -19) + f * least
+    worst = float((np.abs(o.cpu().double().numpy() - ref_o) / bound).max())
+    assert worst <= 1.0, f"{worst} times the bound"
+    assert (np.abs(lse.cpu().double().numpy() - ref_lse) <= dx + 2.0 ** -19 * (1 + np.abs(ref_lse))).all()
+
+
 @pytest.mark.parametrize("factor", [2.0 ** -60, 2.0 ** 14, 2.0 ** 60])
 def test_attention_queries_of_any_range(factor):
     # queries outside f16's range against keys of the inverse one: the logits are ordinary
