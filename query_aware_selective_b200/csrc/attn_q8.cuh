@@ -27,10 +27,13 @@
 // narrow MMA, which is why fp32 stays here; a head of 64 is half the M = 128 that the
 // 8-bit MMAs of attn_q8_tc.cuh take.
 //
-// Bound by HBM for large batches (bf16, heads of 64, 16 sequences x 6.3K keys x 8 heads,
-// 103 MB: 32 us, 3.2 TB/s), by the conversions' and the softmax's issue slots for fp32 on
-// heads of 128 (206 MB: 53 us), by latency for one short sequence (4 heads of 64, 400 keys:
-// 5 us, of which 2 are the launch). A warp streams 16 keys a step through its own ring of
+// Bound by the latency of a warp's own chain (copy, products, exponentials, products), of which
+// the SM holds too few to hide it: bf16 on heads of 64, 16 sequences x 6.3K keys x 8 heads
+// (103 MB), 28 us, 3.7 TB/s, with 14 warps an SM and 44% of the issue slots used, a warp waiting
+// for loads, fixed latencies and shared memory in about equal parts; fp32 on heads of 128
+// (206 MB) 46 us, 4.5 TB/s, with the 8 warps that its registers allow and 39%; 512 fp32 queries
+// at 40% of the issue slots and of the mma.sync pipe each. One short sequence (4 heads of 64,
+// 400 keys) takes 5 us, of which 2 are the launch. A warp streams 16 keys a step through its own ring of
 // three steps in shared memory (16-byte cp.async). The key list of a (sequence, KV head) is
 // split over the 8 warps of a CTA and over the CTAs of a cluster; the parts meet in
 // (distributed) shared memory, so there is no workspace, no counter to clear and no second
