@@ -472,7 +472,11 @@ class EsaDecodeVarlen:
 class EsaDecodeQ8(EsaDecodeVarlen):
     """EsaDecodeVarlen over an 8-bit cache (a CacheQ8), which is the only place the keys and
     values live: a step quantises the new token into it and attends over it, the selection
-    runs on the compressed keys as before."""
+    runs on the compressed keys as before. A compressed key is made from the best row at hand:
+    by step from the new row as it is given, by fill_cache from the row as the cache holds it
+    (nothing else is left of it). The two differ by the compressed rounding of the cache, so a
+    sequence that is filled again after some steps may select a few other tokens than one
+    that goes on."""
 
     def __init__(self, cache: _abi.CacheQ8, hq: int, d_c: int, p: _abi.EsaParams, dtype=torch.bfloat16,
                  per_head: bool = False):
@@ -484,7 +488,8 @@ class EsaDecodeQ8(EsaDecodeVarlen):
 
     def fill_cache(self, wk, lengths):
         """Compress the cached keys [0, lengths[b] - 1) of every sequence (prefill state) as
-        the cache holds them; lengths: host integers."""
+        the cache holds them; lengths: host integers. (Every sequence is read as far as the
+        longest one; rows behind a sequence's own are not used.)"""
         self.cmp.pack_keys(wk)
         step = 1 << 12
         for r0 in range(0, max(int(n) for n in lengths) - 1, step):

@@ -1104,6 +1104,35 @@ def test_prefill_then_decode_over_one_cache(fmt, per_head):
                torch.bfloat16, d)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_decode_compresses_a_row_as_given_or_as_held(fmt):
+    """A step compresses the new key row as it is given, fill_cache the row as the cache holds it,
+    with garbage in the rows behind a sequence."""
+    b, n_cap, hq, hkv, d, dc = 3, 300, 8, 4, 128, 128
+    lens = [40, 299, 130]
+    g = torch.Generator().manual_seed(18)
+    wq, wk = ((torch.randn((hq * d, dc), generator=g) / 32).to(DEV) for _ in range(2))
+    k, v = (torch.randn((b, n_cap, hkv, d), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    q = torch.randn((b, 1, hq, d), generator=g).to(torch.bfloat16).to(DEV)
+    cache = _cache(b, n_cap, hkv, d, fmt, 32)
+    n = torch.tensor(lens, device=DEV)
+    qas.cache_write_q8_varlen(cache, k[:, :max(lens)], v[:, :max(lens)], n, n)
+    dec = pipeline.EsaDecodeQ8(cache, hq, dc, qas.params(16, 64, 50, 2, 45.25))
+    dec.fill_cache(wk, [x + 1 for x in lens])
+    held = qas.cache_read_q8(cache)[0]
+    for s, x in enumerate(lens):
+        want = torch.empty((x, dc), device=DEV)
+        dec.cmp.keys(held[s, :x], out=want)
+        assert torch.equal(dec.k_c[s, :x], want) and not dec.k_c[s, x:].any()
+    new = k[:, -1].contiguous()
+    dec.step(q, new, v[:, -1].contiguous(), wq, wk, n + 1)
+    want = torch.zeros_like(dec.k_c)
+    qas.compress_packed_varlen(new, dec.cmp.wk_p, want, n + 1)
+    qas.device_status()
+    for s, x in enumerate(lens):
+        assert torch.equal(dec.k_c[s, x], want[s, x]) and want[s, x].any()
+
+
 def test_decode_step_in_a_graph_with_lengths_that_differ():
     b, n_cap, hq, hkv, d, dc = 3, 700, 8, 4, 128, 128
     p = qas.params(32, 64, 100, 2, 45.25)
