@@ -51,7 +51,8 @@ constexpr int kQ8Warps = 8, kQ8Threads = kQ8Warps * 32;
 constexpr int kQ8Keys = 16;                     // keys of a warp's step
 constexpr int kQ8Stages = 3;                    // steps of a warp's ring
 // weights: 2^10 at the reference, at most 2^15 (f16: 2^16)
-constexpr float kQ8Head = 10.f, kQ8Unit = 0x1p10f, kQ8Most = 0x1p15f;
+constexpr float kQ8Head = 10.f, kQ8Unit = 0x1p10f;
+constexpr uint32_t kQ8Most = 0x78007800u;       // 2^15 twice, as f16
 
 struct AttnQ8Args {
   const void* q;            // [B, Lq, Hq, D]
@@ -350,7 +351,12 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int c = 0; c < KC; ++c) kr[u][c] = lds128(st + q8_k_off<D>(gid + 8 * u, tig + 4 * c));
-    const float sc_cur = __uint_as_float(lds32(st + 2 * kQ8Keys * D + lane * 4));
+    float sc_k[2], sc_v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      sc_k[u] = __uint_as_float(lds32(st + 2 * kQ8Keys * D + (gid + 8 * u) * 4));
+      sc_v[u] = __uint_as_float(lds32(st + 2 * kQ8Keys * D + (16 + gid + 8 * u) * 4));
+    }
 
     // S^T = Kc Q^T, two chains of half the dims
     float sx[NT][2][4];
@@ -377,31 +383,23 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
     // first, against m as it is; the row maxima (a reduction over 8 lanes) only when one of
     // them says that m has to rise (at once on the first step: m is -inf).
     float ka[2], vb[2];                  // scales of the two keys, the values' times 2^10
-    {
-      const float other = __shfl_xor_sync(0xffffffffu, sc_cur, 16);
-      float ks = sc_cur, vs = lane < 16 ? other : sc_cur;
-      q8_scales(ks, vs);
-      const float own = lane < 16 ? ks : vs * kQ8Unit;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        ka[u] = __shfl_sync(0xffffffffu, own, gid + 8 * u);
-        vb[u] = __shfl_sync(0xffffffffu, own, 16 + gid + 8 * u);
-      }
+    for (int u = 0; u < 2; ++u) {
+      q8_scales(ka[u] = sc_k[u], vb[u] = sc_v[u]);
+      vb[u] *= kQ8Unit;
     }
     const int t0 = s * kQ8Keys;
     const bool cut = t0 + kQ8Keys > n_all;                     // some row does not see some key
     float ex[NT][2][2], wt[NT][2][2];
-    auto weights = [&]() -> float {
-      float top = 0.f;
+    uint32_t wh[NT][2];                                        // the weights as f16, rows 2 tig, 2 tig + 1
+    auto weights = [&]() -> bool {                             // whether one is above kQ8Most
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < 2; ++u)
             ex[nt][u][j] = fast_exp2(fmaf(sx[nt][0][2 * u + j] + sx[nt][1][2 * u + j], ka[u] * xs[nt][j], -m[nt][j]));
-            wt[nt][u][j] = ex[nt][u][j] * vb[u];
-          }
       if (cut) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -409,14 +407,21 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              if (t0 + gid + 8 * u >= lim[nt][j]) ex[nt][u][j] = wt[nt][u][j] = 0.f;
+              if (t0 + gid + 8 * u >= lim[nt][j]) ex[nt][u][j] = 0.f;
       }
+      uint32_t top = 0u;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        top = fmaxf(fmaxf(top, fmaxf(wt[nt][0][0], wt[nt][0][1])), fmaxf(wt[nt][1][0], wt[nt][1][1]));
-      return top;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          wt[nt][u][0] = ex[nt][u][0] * vb[u];
+          wt[nt][u][1] = ex[nt][u][1] * vb[u];
+          wh[nt][u] = f16x2_rn(wt[nt][u][0], wt[nt][u][1]);
+          asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(wh[nt][u]));       // (not NaN, where one of the two is not)
+        }
+      return ((top + 0x80008000u - kQ8Most - 0x00010001u) & 0x80008000u) != 0u;
     };
-    if (__any_sync(0xffffffffu, weights() > kQ8Most)) {
+    if (__any_sync(0xffffffffu, weights())) {
       const float lv[2] = {fast_log2(vb[0]) - kQ8Head, fast_log2(vb[1]) - kQ8Head};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -455,10 +460,9 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 && D == 64 ? 2 : 1) attn_q
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) l[nt][j] += ex[nt][u][j];
-        const uint32_t h = f16x2_rn(wt[nt][u][0], wt[nt][u][1]);
-        wf[nt][u] = movmatrix_t(h);
+        wf[nt][u] = movmatrix_t(wh[nt][u]);
         if constexpr (F32) {
-          const float2 hf = f16x2_to_float2(h);
+          const float2 hf = f16x2_to_float2(wh[nt][u]);
           wl[nt][u] = movmatrix_t(f16x2_rn(wt[nt][u][0] - hf.x, wt[nt][u][1] - hf.y));
         }
       }
