@@ -496,6 +496,9 @@ class CacheQ8:
 def cache_q8(batch: int, n_cap: int, hkv: int, head_dim: int, dtype: torch.dtype = torch.float8_e4m3fn,
              block: int = 64, device="cuda") -> CacheQ8:
     """A new, empty CacheQ8 (codes and scales zero)."""
+    if block not in (16, 32, 64, 128):
+        raise ValueError("block must be 16, 32, 64 or 128")
+
     def codes():
         return torch.zeros((batch, n_cap, hkv, head_dim), dtype=torch.uint8, device=device).view(dtype)
 

@@ -196,3 +196,9 @@ def test_import_needs_no_private_name_of_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(qas.__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("block", [0, -16, 48, 256])
+def test_new_caches_of_a_wrong_block_are_refused(block):
+    with pytest.raises(ValueError, match="block must be"):
+        qas.cache_q8(1, 64, 2, 64, block=block, device="cpu")
