@@ -471,7 +471,8 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  * times the scale of its value):
  *   bf16, head_dim 128: codes exact; an element of a query to 2^-21 (e4m3) or 2^-20 (int8) of
  *     its row's largest, so that bf16's own 8 bits are whole down to 2^-12 of it; weights to
- *     2^-13 of themselves and 2^-26 of the largest of 128 keys (e4m3), to 2^-28 of that (int8)
+ *     2^-17 of themselves and 2^-30 of the largest of 128 keys (e4m3, up to 8 query rows a KV
+ *     head), to 2^-13 and 2^-26 (e4m3, more rows), to 2^-28 of that largest (int8)
  *   bf16, head_dim 64: codes exact; queries exact down to 2^-30 of the row's largest; weights to
  *     2^-11 of themselves and 2^-35 of the largest
  *   fp32: codes exact; queries and weights to 2^-21 of themselves (the ends as above)

@@ -9,7 +9,10 @@
 // kind::f8f6f4 for e4m3 (fp32 sums), kind::i8 for int8 (exact 32-bit sums). Queries and
 // weights go in as P pieces of 8 bits, each its own column:
 //   e4m3: piece p = e4m3(16^p (x - pieces before)), 4 significant bits each: two for a bf16
-//         query, three for a weight (relative 2^-13)
+//         query, three for a weight (relative 2^-13), four with up to 8 query rows (2^-17: the
+//         columns are there anyway, N is a multiple of 16, and the rows are few; 16 sequences
+//         of 4 rows 38.9 -> 39.1 us. With 20 rows the fourth took 40.4 -> 42.2 us, with 400
+//         71 -> 75)
 //   int8: digits of 7 bits of an integer: three for a query (its row's largest is 2^19 to
 //         2^20), four for a weight (its tile's largest is 2^27)
 // (a query's element to 2^-21 or 2^-20 of its row's largest: bf16's 8 bits are whole down to
@@ -18,8 +21,8 @@
 // WR + r is piece p of row r of row group rg.
 // Weights are taken relative to their key tile's own maximum (of 128 keys), and a tile's O
 // is drained from TMEM into fp32 registers and scaled there: the range of 8-bit pieces
-// then only has to span one tile (a weight is rounded to 2^-26 (e4m3) or 2^-28 (int8) of its
-// tile's largest at worst; three int8 digits, 2^-21, showed in dims where the largest
+// then only has to span one tile (a weight is rounded to 2^-26 or 2^-30 (e4m3) or 2^-28 (int8)
+// of its tile's largest at worst; three int8 digits, 2^-21, showed in dims where the largest
 // weight's value is next to zero), and nothing in TMEM is ever rescaled. The maximum is
 // that of x_j + log2 b_j, and a weight e_j b_j with e_j = 2^(x_j - maximum); l sums the e_j (as in
 // attn_q8.cuh: b_j spans 2^198, which a weight does not hold).
@@ -58,7 +61,7 @@ constexpr int kQtMaxCluster = 8;
 template <int FMT, int WR, int RG, int TG>
 struct QtShape {
   static constexpr int RT = WR * RG;
-  static constexpr int NQ = FMT == kQ8E4M3 ? 2 : 3, NW = FMT == kQ8E4M3 ? 3 : 4;   // pieces of a query, of a weight
+  static constexpr int NQ = FMT == kQ8E4M3 ? 2 : 3, NW = FMT == kQ8E4M3 && RT > 8 ? 3 : 4;   // pieces of a query, of a weight
   static constexpr int N = (NW * RT + 15) / 16 * 16;          // MMA columns (M = 128: a multiple of 16)
   static constexpr int kThreads = (4 * RG * TG + 3) * 32;
   static constexpr int kStages = RT <= 8 ? 6 : 5;
@@ -74,7 +77,7 @@ struct QtShape {
   static constexpr uint32_t kSmem = kRing + kStages * 512;
   // a warpgroup sees every phase of the barriers it waits for
   static_assert(kStages % TG == 0 && NS % TG == 0 && 2 % TG == 0, "stages and buffers that the tile groups share");
-  static_assert((WR == 4 && RG == 1) || (WR == 8 && N - NW * RT <= 8), "columns of a weight's stores");
+  static_assert((WR == 4 && RG == 1 && NW == 4) || (WR == 8 && N - NW * RT <= 8), "columns of a weight's stores");
   static_assert(kSmem <= 232448 && (NS + 2) * N <= 512 && (kMl * 4) % 16 == 0 && (kO * 4) % 16 == 0, "does not fit an SM");
 };
 
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__((QtShape<FMT, WR, RG, TG>::kThreads), 1) attn_
       }
       const uint32_t wb = base + Sh::kW + (j & 1) * N * 128 + key * 16;
       if constexpr (WR == 4) {
-        st_shared_v4(wb, ww[0][0], ww[1][0], ww[2][0], NW == 4 ? ww[3][0] : 0u);
+        st_shared_v4(wb, ww[0][0], ww[1][0], ww[2][0], ww[3][0]);
       } else {
         // (the last row group's pieces are followed by the columns that belong to none)
 #pragma unroll

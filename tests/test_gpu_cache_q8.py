@@ -656,9 +656,11 @@ def test_attention_scales_far_apart():
 
 
 # What the kernels on the codes promise of a weight and of a query, by (dtype, head dim, format):
-# u, the relative rounding of a weight: 2^-13 for three e4m3 pieces of 4 significant bits, none
-#    for int8 digits, 2^-11 for an f16, 2^-21 for two (fp32 queries);
-# f, its absolute rounding in units of its tile's largest: 2^-26, 2^-28, and 2^-35 for f16;
+# u, the relative rounding of a weight: 2^-13 for three e4m3 pieces of 4 significant bits, 2^-17 for
+#    four (up to 8 rows a KV head), none for int8 digits, 2^-11 for an f16, 2^-21 for two (fp32
+#    queries);
+# f, its absolute rounding in units of its tile's largest: 2^-26 (of the fourth piece 2^-30), 2^-28,
+#    and 2^-35 for f16;
 # e, the rounding of a query element in units of its row's largest: two e4m3 pieces end at steps
 #    of 2^-9 16^-1 for a largest of 2^7 or more, so half of 2^-13 in 2^7: 2^-21; three digits
 #    round to a whole number with a largest of 2^19 or more: 2^-20; an f16 has steps of 2^-24
@@ -717,10 +719,12 @@ def test_attention_weights_keep_their_bits(dtype, d, fmt, group):
     qas.device_status()
     ref_o, _, big, xmax, least = _reference(q, kv, vv, [n - 1] * b, idx, cnt, 0, n)
     u, f, e = PROMISED[dtype, d, fmt]
+    if (dtype, d, fmt) == (torch.bfloat16, 128, "e4m3") and group <= 8:
+        u, f = 2.0 ** -17, 2.0 ** -30
     dx = xmax[..., None] * (8 * 2.0 ** -24 + e)              # one product a logit, its scalings, the query's rounding
     bound = torch.finfo(dtype).eps / 2 * np.abs(ref_o) + big * (u + 2 * dx + 2.0 ** -19) + f * least
     # (of each KV head's first query the rounding of the output leaves room to see a weight's)
-    assert np.median((bound / big)[:, :, ::group]) < 2.0 ** (-10 if u else -14)
+    assert np.median((bound / big)[:, :, ::group]) < 2.0 ** (-10 if u > 2.0 ** -14 else -14)
     worst = float((np.abs(o.cpu().double().numpy() - ref_o) / bound).max())
     assert worst <= 1.0, f"{worst} times the bound"
 
