@@ -35,7 +35,7 @@
 // cluster sends every other its part of their dims and merges its own.
 //
 // Bound by HBM with up to 8 rows: 16 sequences x 6.3K keys x 8 heads (206 MB, a CTA per
-// sequence and head) take 38.6 us, 5.3 TB/s; the loop alone streams at 6.4 TB/s, 2.7 us go
+// sequence and head) take 39.2 us (int8 38.8), 5.3 TB/s; the loop alone streams at 6.4 TB/s, 2.7 us go
 // to the launch, the queries and the first keys, 1.8 us to the last tile and the merge, and
 // 128 units leave 20 of 148 SMs idle. One CTA of six stages an SM beat two of three, 39.7
 // against 42 us. With more rows bound by the softmax warps' issue slots: 20 rows x 24 units

@@ -151,8 +151,9 @@ __device__ __forceinline__ void ld_global_32(const void* p, bool wide, uint32_t*
 // once: load everything, take the maximum, scale, round, store. Bound by HBM (and by
 // launch and one memory latency for a single token). grid (blocks * 2 Hkv, B), heads
 // fastest: the CTAs that share rows run together, so DRAM pages are read whole.
-// 32768 tokens of 8 heads of 128 (201 MB): 33.7 us, 5.98 TB/s, with 32-byte loads; 39.1 us
-// with 16-byte loads of 8 elements a row and thread.
+// 32768 tokens of 8 heads of 128 (201 MB): 31.2 us, 6.4 TB/s, of fp32 rows (336 MB) 50.2 us,
+// 6.7 TB/s. (16-byte loads of 8 elements a row and thread: 39.1 us where these 32-byte loads
+// took 33.7.)
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(256) cache_write_q8_kernel(const CacheWriteArgs a) {
   constexpr int TPR = D / 16;                      // threads of a row
