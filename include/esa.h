@@ -466,9 +466,12 @@ esa_status_t esa_cache_read_q8(esa_cache_q8_t cache, int64_t start, int64_t rows
  * (esa_cache_write_q8 writes none); a query row with a NaN or an infinity gives a row of NaN.
  * hq is a multiple of hkv; no limit on their ratio. Entries of idx may repeat (count may be up
  * to topk whatever the length of the middle); entries outside the cache are clamped into it.
- * Precision. Sums are fp32 or exact. Which rounding the queries and the softmax weights get
- * goes by dtype, head_dim, format and the number of query rows (a weight here is that of a key
- * times the scale of its value):
+ * Logits have to fit fp32 (beyond it a row becomes NaN).
+ * Precision. Sums are fp32 or exact; so is a weight's exponent, log2 of its value's scale
+ * included, of whose size 2^-24 comes on top of the below. Which rounding the queries and the
+ * softmax weights get goes by dtype, head_dim, format and the number of query rows (a weight
+ * here is that of a key times the scale of its value; a query row whose largest element is under
+ * 2^-81 is rounded as one of 2^-81):
  *   bf16, head_dim 128: codes exact; an element of a query to 2^-21 (e4m3) or 2^-20 (int8) of
  *     its row's largest, so that bf16's own 8 bits are whole down to 2^-12 of it; weights to
  *     2^-17 of themselves and 2^-30 of the largest of 128 keys (e4m3, up to 8 query rows a KV
